@@ -7,6 +7,7 @@
 #include <cstring>
 #include <string>
 
+#include "bwd.cuh"
 #include "common.cuh"
 
 namespace paro {
@@ -15,7 +16,8 @@ cudaError_t launch_attn_sm100(const void* q, const void* k, const void* v, pa_dt
                               int k_max, const float* qs, const float* ks, const float* vs,
                               float p_levels, void* out, int32_t* status, bool permuted,
                               cudaStream_t s, const void* k_pool = nullptr,
-                              const void* v_pool = nullptr, pa_dtype pool_dtype = PA_F32);
+                              const void* v_pool = nullptr, pa_dtype pool_dtype = PA_F32,
+                              float* lse = nullptr);
 bool attn_sm100_supports(pa_dtype dt, const Grid& g);
 }  // namespace paro
 
@@ -490,6 +492,264 @@ pa_status pa_round_bf16(const float* x, void* y, int64_t n, void* stream) {
   PA_REQUIRE(aligned16(x) && aligned16(y), "x and y must be 16-byte aligned");
   PA_REQUIRE(n <= ((int64_t)1 << 40), "n=%lld too large", (long long)n);
   return cuda_status(paro::launch_round_bf16(x, y, n, (cudaStream_t)stream), "pa_round_bf16 launch");
+}
+
+// ------------------------------------------------------ rotary positions --
+
+// Why a rotation is malformed, or NULL.
+static const char* rope_fault(const pa_rope& r) {
+  int64_t pairs = 0, floats = 0;
+  for (int a = 0; a < 3; ++a) {
+    if (r.extent[a] < 1) return "rope.extent must be >= 1 on every axis";
+    if (r.pairs[a] < 0 || r.pairs[a] > 64) return "rope.pairs must be in [0, 64] on every axis";
+    pairs += r.pairs[a];
+    floats += (int64_t)r.extent[a] * 2 * (r.pairs[a] + 8);
+  }
+  if (pairs < 1 || pairs > 64) return "rope.pairs must sum to 1 .. 64";
+  if (r.interleaved != 0 && r.interleaved != 1) return "rope.interleaved must be 0 or 1";
+  if (floats > ((int64_t)1 << 31)) return "the rope table exceeds 2^31 floats";
+  return nullptr;
+}
+
+int64_t pa_rope_table_floats(pa_rope rope) {
+  if (rope_fault(rope) != nullptr) return -1;
+  paro::RopeTab tab;
+  return 2 * paro::make_rope_tab(rope, &tab);
+}
+
+pa_status pa_rope_table(pa_rope rope, double theta, const double first[3], const double step[3],
+                        float* table, void* stream) {
+  const char* why = rope_fault(rope);
+  PA_REQUIRE(why == nullptr, "%s", why);
+  PA_REQUIRE(first && step && table, "first, step and table must be non-NULL");
+  PA_REQUIRE(aligned16(table), "table must be 16-byte aligned");
+  PA_REQUIRE(std::isfinite(theta) && theta > 0.0, "theta must be finite and > 0");
+  for (int a = 0; a < 3; ++a)
+    PA_REQUIRE(std::isfinite(first[a]) && std::isfinite(step[a]), "first and step must be finite");
+  paro::RopeTab tab;
+  paro::make_rope_tab(rope, &tab);
+  return cuda_status(paro::launch_rope_table(tab, theta, first, step, table, (cudaStream_t)stream),
+                     "pa_rope_table launch");
+}
+
+static pa_status row_stride(const char* name, const int64_t* given, const paro::Grid& g,
+                            pa_dtype dtype, paro::RowStride* out) {
+  if (given == nullptr) {
+    *out = paro::RowStride{(int64_t)g.heads * g.N * g.d, (int64_t)g.N * g.d, g.d};
+    return PA_OK;
+  }
+  const int64_t e = dtype == PA_F32 ? 4 : 8;
+  for (int i = 0; i < 3; ++i)
+    PA_REQUIRE(given[i] >= 0 && given[i] < ((int64_t)1 << 40) && given[i] % e == 0,
+               "%s[%d]=%lld must be >= 0 and a multiple of 16 bytes", name, i, (long long)given[i]);
+  *out = paro::RowStride{given[0], given[1], given[2]};
+  return PA_OK;
+}
+
+static pa_status rope_common(const pa_rope& rope, const paro::Grid& g, const float* table,
+                             paro::RopeTab* tab) {
+  const char* why = rope_fault(rope);
+  PA_REQUIRE(why == nullptr, "%s", why);
+  PA_REQUIRE(rope.pairs[0] + rope.pairs[1] + rope.pairs[2] <= g.d / 2,
+             "rope.pairs sum to %d, more than d/2 = %d",
+             rope.pairs[0] + rope.pairs[1] + rope.pairs[2], g.d / 2);
+  PA_REQUIRE(table && aligned16(table), "table must be non-NULL and 16-byte aligned");
+  paro::make_rope_tab(rope, tab);
+  return PA_OK;
+}
+
+static pa_status rope_covers(const pa_rope& rope, const paro::Grid& g) {
+  PA_REQUIRE(rope.extent[0] >= g.F && rope.extent[1] >= g.H && rope.extent[2] >= g.W,
+             "rope.extent (%d, %d, %d) does not cover the grid (%d, %d, %d)", rope.extent[0],
+             rope.extent[1], rope.extent[2], g.F, g.H, g.W);
+  return PA_OK;
+}
+
+pa_status pa_rope_apply(const void* x, const int64_t* x_stride, void* y, const int64_t* y_stride,
+                        pa_dtype dtype, pa_shape shape, pa_rope rope, const float* table,
+                        const int32_t* positions, int32_t positions_batched, uint32_t flags,
+                        int32_t* dev_status, void* stream) {
+  paro::Grid g;
+  paro::RopeTab tab;
+  paro::RowStride xs, ys;
+  pa_status st = check_float_dtype(dtype);
+  if (st != PA_OK) return st;
+  if ((st = make_grid(shape, nullptr, false, &g)) != PA_OK) return st;
+  if ((st = rope_common(rope, g, table, &tab)) != PA_OK) return st;
+  PA_REQUIRE(x && y, "x and y must be non-NULL");
+  PA_REQUIRE(aligned16(x) && aligned16(y), "x and y must be 16-byte aligned");
+  if ((st = row_stride("x_stride", x_stride, g, dtype, &xs)) != PA_OK) return st;
+  if ((st = row_stride("y_stride", y_stride, g, dtype, &ys)) != PA_OK) return st;
+  PA_REQUIRE(x != y || (xs.batch == ys.batch && xs.head == ys.head && xs.token == ys.token),
+             "y == x needs equal strides");
+  PA_REQUIRE((flags & ~PA_ROPE_INVERSE) == 0, "unknown flags 0x%x", flags);
+  PA_REQUIRE(positions_batched == 0 || positions_batched == 1, "positions_batched must be 0 or 1");
+  if (positions == nullptr && (st = rope_covers(rope, g)) != PA_OK) return st;
+  if (g.B > 65535) return fail(PA_ERR_UNSUPPORTED, "B=%d exceeds 65535", g.B);
+  return cuda_status(paro::launch_rope(x, xs, y, ys, dtype, g, tab, rope.interleaved != 0, table,
+                                       positions, positions_batched ? (int64_t)g.N * 3 : 0,
+                                       (flags & PA_ROPE_INVERSE) != 0, dev_status,
+                                       (cudaStream_t)stream),
+                     "pa_rope_apply launch");
+}
+
+pa_status pa_rope_reorder(const void* x, const int64_t* x_stride, void* x_perm, pa_dtype dtype,
+                          pa_shape shape, const int8_t* perms, pa_rope rope, const float* table,
+                          float* pool, void* stream) {
+  paro::Grid g;
+  paro::RopeTab tab;
+  paro::RowStride xs;
+  pa_status st = check_float_dtype(dtype);
+  if (st != PA_OK) return st;
+  if ((st = make_grid(shape, perms, true, &g)) != PA_OK) return st;
+  if ((st = rope_common(rope, g, table, &tab)) != PA_OK) return st;
+  if ((st = rope_covers(rope, g)) != PA_OK) return st;
+  PA_REQUIRE(x && x_perm, "x and x_perm must be non-NULL");
+  PA_REQUIRE(aligned16(x) && aligned16(x_perm), "x and x_perm must be 16-byte aligned");
+  if ((st = row_stride("x_stride", x_stride, g, dtype, &xs)) != PA_OK) return st;
+  if ((int64_t)g.B * g.heads > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "B*heads=%lld exceeds 65535", (long long)g.B * g.heads);
+  return cuda_status(paro::launch_rope_reorder(x, xs, x_perm, dtype, g, tab, rope.interleaved != 0,
+                                               table, pool, (cudaStream_t)stream),
+                     "pa_rope_reorder launch");
+}
+
+// -------------------------------------------------------------- training --
+
+pa_status pa_block_sparse_attn_lse(const void* q, const void* k, const void* v, pa_dtype dtype,
+                                   uint32_t flags, pa_shape shape, const int8_t* perms,
+                                   const int32_t* idx, const int32_t* counts, int32_t k_max,
+                                   void* out, float* lse, int32_t* dev_status, void* stream) {
+  paro::Grid g;
+  pa_status st = make_grid(shape, perms, true, &g);
+  if (st != PA_OK) return st;
+  if (dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "dtype %d: training attention takes PA_BF16", (int)dtype);
+  PA_REQUIRE(q && k && v && out && lse, "q, k, v, out and lse must be non-NULL");
+  PA_REQUIRE(idx || k_max == 0, "idx must be non-NULL when k_max > 0");
+  PA_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(out),
+             "q, k, v and out must be 16-byte aligned");
+  PA_REQUIRE(k_max >= 0 && k_max <= g.NB, "k_max=%d must be in [0, NB=%d]", k_max, g.NB);
+  PA_REQUIRE((flags & ~PA_ATTN_PERMUTED) == 0, "unknown flags 0x%x", flags);
+  const bool permuted = (flags & PA_ATTN_PERMUTED) != 0;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int64_t rows = (int64_t)g.B * g.heads * g.N;
+  cudaError_t e;
+  if (k_max == 0) {
+    e = cudaMemsetAsync(out, 0, (size_t)rows * g.d * 2, s);
+    if (e == cudaSuccess) e = paro::launch_fill(lse, -INFINITY, rows, s);
+  } else if (paro::attn_sm100_supports(dtype, g)) {
+    e = paro::launch_attn_sm100(q, k, v, dtype, g, idx, counts, k_max, nullptr, nullptr, nullptr,
+                                127.f, out, dev_status, permuted, s, nullptr, nullptr, PA_F32, lse);
+  } else {
+    e = paro::launch_attn_mma(q, k, v, dtype, g, idx, counts, k_max, out, dev_status, permuted, s,
+                              nullptr, nullptr, lse);
+  }
+  return cuda_status(e, "pa_block_sparse_attn_lse launch");
+}
+
+namespace {
+// The backward pass's workspace: dO permuted, row statistics, transposed
+// kept lists, each at a multiple of 256 bytes.
+struct BwdLayout {
+  int64_t stats, mask, bytes;
+  int words;
+};
+BwdLayout bwd_layout(const paro::Grid& g) {
+  auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+  const int64_t rows = (int64_t)g.B * g.heads * g.Np;
+  BwdLayout l;
+  l.words = (g.NB + 31) / 32;
+  l.stats = up(rows * g.d * 2);
+  l.mask = l.stats + up(rows * 8);
+  l.bytes = l.mask + up((int64_t)g.B * g.heads * g.NB * l.words * 4);
+  return l;
+}
+pa_status bwd_limits(const paro::Grid& g) {
+  if (g.NB > 65535 || (int64_t)g.B * g.heads > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "NB=%d or B*heads=%lld exceeds 65535", g.NB,
+                (long long)g.B * g.heads);
+  return PA_OK;
+}
+}  // namespace
+
+int64_t pa_block_sparse_attn_backward_workspace(pa_shape shape) {
+  paro::Grid g;
+  if (make_grid(shape, nullptr, false, &g) != PA_OK || bwd_limits(g) != PA_OK) return -1;
+  return bwd_layout(g).bytes;
+}
+
+pa_status pa_block_sparse_attn_backward(const void* dout, const void* q, const void* k,
+                                        const void* v, const void* out, const float* lse,
+                                        const float* dlse, pa_dtype dtype, pa_shape shape,
+                                        const int8_t* perms, const int32_t* idx,
+                                        const int32_t* counts, int32_t k_max, void* dq, void* dk,
+                                        void* dv, void* workspace, int64_t workspace_bytes,
+                                        int32_t* dev_status, void* stream) {
+  paro::Grid g;
+  pa_status st = make_grid(shape, perms, true, &g);
+  if (st != PA_OK) return st;
+  if ((st = bwd_limits(g)) != PA_OK) return st;
+  if (dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "dtype %d: training attention takes PA_BF16", (int)dtype);
+  PA_REQUIRE(dout && q && k && v && out && lse && dq && dk && dv,
+             "dout, q, k, v, out, lse, dq, dk and dv must be non-NULL");
+  PA_REQUIRE(idx || k_max == 0, "idx must be non-NULL when k_max > 0");
+  PA_REQUIRE(aligned16(dout) && aligned16(q) && aligned16(k) && aligned16(v) && aligned16(out) &&
+                 aligned16(dq) && aligned16(dk) && aligned16(dv),
+             "dout, q, k, v, out, dq, dk and dv must be 16-byte aligned");
+  PA_REQUIRE(k_max >= 0 && k_max <= g.NB, "k_max=%d must be in [0, NB=%d]", k_max, g.NB);
+  const BwdLayout l = bwd_layout(g);
+  PA_REQUIRE(workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,
+             "workspace must be non-NULL and 256-byte aligned");
+  PA_REQUIRE(workspace_bytes >= l.bytes, "workspace of %lld bytes, %lld needed",
+             (long long)workspace_bytes, (long long)l.bytes);
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  paro::BwdArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.dop = reinterpret_cast<__nv_bfloat16*>(w);
+  a.stats = reinterpret_cast<float2*>(w + l.stats);
+  a.mask = reinterpret_cast<uint32_t*>(w + l.mask);
+  a.words = l.words;
+  a.idx = idx;
+  a.counts = counts;
+  a.k_max = k_max;
+  a.dq = static_cast<__nv_bfloat16*>(dq);
+  a.dk = static_cast<__nv_bfloat16*>(dk);
+  a.dv = static_cast<__nv_bfloat16*>(dv);
+  a.status = dev_status;
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = paro::launch_bwd_prep(out, dout, lse, dlse, a, g, s);
+  if (e == cudaSuccess) e = paro::launch_bwd_mma(a, g, s);
+  return cuda_status(e, "pa_block_sparse_attn_backward launch");
+}
+
+// --------------------------------------------------------------- serving --
+
+pa_status pa_query_attn(const void* q, const void* k, const void* v, const float* k_pool,
+                        pa_dtype dtype, pa_shape shape, int32_t q_group, int32_t M,
+                        int32_t k_keep, const int32_t* lengths, void* out, int32_t* idx,
+                        float* lse, int32_t* dev_status, void* stream) {
+  paro::Grid g;
+  pa_status st = check_float_dtype(dtype);
+  if (st != PA_OK) return st;
+  if ((st = make_grid(shape, nullptr, false, &g)) != PA_OK) return st;
+  PA_REQUIRE(q && k && v && k_pool && out && idx, "q, k, v, k_pool, out and idx must be non-NULL");
+  PA_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(k_pool) && aligned16(out),
+             "q, k, v, k_pool and out must be 16-byte aligned");
+  PA_REQUIRE(q_group >= 1 && M >= 1, "q_group=%d and M=%d must be >= 1", q_group, M);
+  PA_REQUIRE(k_keep >= 1 && k_keep <= g.NB, "k_keep=%d must be in [1, NB=%d]", k_keep, g.NB);
+  if (g.NB > paro::kTopkMaxNB)
+    return fail(PA_ERR_UNSUPPORTED, "NB=%d exceeds %d (a row's keys must fit in shared memory)",
+                g.NB, paro::kTopkMaxNB);
+  const int64_t most = (int64_t)1 << 27;
+  if ((int64_t)g.B * g.heads > most / q_group || (int64_t)g.B * g.heads * q_group > most / M)
+    return fail(PA_ERR_UNSUPPORTED, "B*heads*q_group*M exceeds 2^27 query rows");
+  return cuda_status(paro::launch_query_attn(q, k, v, k_pool, dtype, g, q_group, M, k_keep, lengths,
+                                             out, idx, lse, dev_status, (cudaStream_t)stream),
+                     "pa_query_attn launch");
 }
 
 }  // extern "C"

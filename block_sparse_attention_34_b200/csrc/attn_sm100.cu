@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       int k_max, float scale_log2, __nv_bfloat16* __restrict__ out,
                       int32_t* __restrict__ status, const StallTest st,
                       const void* __restrict__ k_pool, const void* __restrict__ v_pool,
-                      int pool_bf16) {
+                      int pool_bf16, float* __restrict__ lse) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // the operand tiles need 1024-byte alignment (the swizzle pattern repeats
   // every 8 rows of 128 bytes); dynamic shared memory starts at the window
@@ -662,9 +662,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // group g writes output columns 64g .. 64g+63 of the row at the natural
     // position of its token
     const int p = i * kBlock + r;
-    __nv_bfloat16* orow = p < g.N ? out + (bh * (int64_t)g.N + natural_index(g, order, p)) * kD
-                                  : nullptr;
+    const int64_t nat = p < g.N ? bh * (int64_t)g.N + natural_index(g, order, p) : -1;
+    __nv_bfloat16* orow = nat >= 0 ? out + nat * kD : nullptr;
     if (run && n_tiles == 0) {
+      if (lse != nullptr && nat >= 0 && grp == 0) lse[nat] = -INFINITY;
       if (orow != nullptr)
         for (int c = 0; c < 8; ++c)
           reinterpret_cast<uint4*>(orow + grp * 64)[c] = make_uint4(0, 0, 0, 0);
@@ -680,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lt = (m0 == -INFINITY ? 0.f : lsum[r] * ex2(m0 - m)) +
                          (m1 == -INFINITY ? 0.f : lsum[128 + r] * ex2(m1 - m));
         inv = lt > 0.f ? 1.f / lt : 0.f;
+        if (lse != nullptr && nat >= 0 && grp == 0) lse[nat] = row_lse(m, lt);
       }
       // every P V has completed once the last one's commit fired
       if (okm) okm = warp_wait(pv_done(n_tiles - 1), ring_par(n_tiles - 1), ctl);
@@ -721,7 +723,8 @@ cudaError_t launch_typed(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
                          const CUtensorMap& mkp, const CUtensorMap& mvp, const void* q,
                          const void* k, const void* v, const Grid& g, const int32_t* idx,
                          const int32_t* counts, int k_max, void* out, int32_t* status,
-                         cudaStream_t s, const void* k_pool, const void* v_pool, int pool_bf16) {
+                         cudaStream_t s, const void* k_pool, const void* v_pool, int pool_bf16,
+                         float* lse) {
   if (kComp && g.NB > kCompMaxNB) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attn_sm100_kernel<kTma, kComp>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
@@ -731,7 +734,7 @@ cudaError_t launch_typed(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   attn_sm100_kernel<kTma, kComp><<<grid, kThreads, kSmemBytes, s>>>(
       mq, mk, mv, mkp, mvp, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
       static_cast<const __nv_bfloat16*>(v), g, idx, counts, k_max, scale_log2,
-      static_cast<__nv_bfloat16*>(out), status, stall_test(), k_pool, v_pool, pool_bf16);
+      static_cast<__nv_bfloat16*>(out), status, stall_test(), k_pool, v_pool, pool_bf16, lse);
   return cudaGetLastError();
 }
 
@@ -747,7 +750,7 @@ cudaError_t launch_attn_sm100(const void* q, const void* k, const void* v, pa_dt
                               int k_max, const float* qs, const float* ks, const float* vs,
                               float p_levels, void* out, int32_t* status, bool permuted,
                               cudaStream_t s, const void* k_pool, const void* v_pool,
-                              pa_dtype pool_dtype) {
+                              pa_dtype pool_dtype, float* lse) {
   if (!attn_sm100_supports(dt, g)) return cudaErrorInvalidValue;
   const bool comp = k_pool != nullptr && v_pool != nullptr;
   if (comp && dt != PA_BF16) return cudaErrorInvalidValue;
@@ -767,14 +770,14 @@ cudaError_t launch_attn_sm100(const void* q, const void* k, const void* v, pa_dt
         !encode_tile_map(&mv, v, rows, kD, 2, 64, kBlock))
       return cudaErrorInvalidValue;
     return comp ? launch_typed<true, true>(mq, mk, mv, mkp, mvp, q, k, v, g, idx, counts, k_max,
-                                           out, status, s, k_pool, v_pool, pool_bf16)
+                                           out, status, s, k_pool, v_pool, pool_bf16, lse)
                 : launch_typed<true, false>(mq, mk, mv, mkp, mvp, q, k, v, g, idx, counts, k_max,
-                                            out, status, s, nullptr, nullptr, 0);
+                                            out, status, s, nullptr, nullptr, 0, lse);
   }
   return comp ? launch_typed<false, true>(mq, mk, mv, mkp, mvp, q, k, v, g, idx, counts, k_max,
-                                          out, status, s, k_pool, v_pool, pool_bf16)
+                                          out, status, s, k_pool, v_pool, pool_bf16, lse)
               : launch_typed<false, false>(mq, mk, mv, mkp, mvp, q, k, v, g, idx, counts, k_max,
-                                           out, status, s, nullptr, nullptr, 0);
+                                           out, status, s, nullptr, nullptr, 0, lse);
 }
 
 }  // namespace paro

@@ -1,0 +1,39 @@
+// What the backward pass's kernel files share: the launch arguments and the
+// check of a kept list.
+#pragma once
+
+#include "common.cuh"
+
+namespace paro {
+
+struct BwdArgs {
+  const __nv_bfloat16 *q, *k, *v;  // permuted [B*heads, Np, d]
+  __nv_bfloat16* dop;              // workspace: dO in the permuted order
+  float2* stats;                   // workspace: (lse log2 e, D) of each permuted row
+  uint32_t* mask;                  // workspace: [B*heads, NB, words], bit i of row j: i keeps j
+  int words;
+  const int32_t *idx, *counts;
+  int k_max;
+  __nv_bfloat16 *dq, *dk, *dv;  // natural order
+  int32_t* status;
+};
+
+// Whether a kept list is well formed (count in [0, k_max], entries ascending
+// in [0, NB)): one warp, the same answer in every lane.
+__device__ __forceinline__ bool list_ok(const int32_t* __restrict__ ids, int cnt, int k_max,
+                                        int NB, int lane) {
+  bool bad = cnt < 0 || cnt > k_max;
+  if (!bad)
+    for (int e = lane; e < cnt; e += 32) {
+      const int j = __ldg(ids + e);
+      const int prev = e > 0 ? __ldg(ids + e - 1) : -1;
+      bad |= j <= prev || j >= NB;
+    }
+  return !__any_sync(0xffffffffu, bad);
+}
+
+cudaError_t launch_bwd_prep(const void* out, const void* dout, const float* lse,
+                            const float* dlse, const BwdArgs& a, const Grid& g, cudaStream_t s);
+cudaError_t launch_bwd_mma(const BwdArgs& a, const Grid& g, cudaStream_t s);
+
+}  // namespace paro

@@ -41,6 +41,18 @@ struct Grid {
   int8_t perm[kMaxHeads];
 };
 
+// Rotary positions (rope.cu): for each axis its table rows, its pairs, its
+// first pair, the groups of four pairs of a table row, and where its rows
+// start (in pairs).
+struct RopeTab {
+  int32_t extent[3], pairs[3], start[3], groups[3];
+  int64_t offset[3];
+};
+// Element strides of a [B, heads, N, d] tensor whose rows are contiguous.
+struct RowStride {
+  int64_t batch, head, token;
+};
+
 // Test hook of the bounded waits (pa_test_inject_v_stall): the V-tile
 // loader of CTA (cta_x, cta_y) of the tcgen05 bf16 attention kernel skips
 // kept tile `tile` (no copy, no arrival), and every bounded wait of that
@@ -80,6 +92,12 @@ __device__ __forceinline__ int natural_index(const Grid& g, int order, int p) {
   const int h1 = rem / sw;
   const int w1 = rem - h1 * sw;
   return (a * tf + f1) * HW + (b * th + h1) * g.W + c * tw + w1;
+}
+
+// Log-sum-exp of a row from its maximum m (log2 units) and its sum l of
+// 2^(s - m); -inf for a row without keys.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // First error wins; never traps.
@@ -150,7 +168,26 @@ cudaError_t launch_quantize(const void* x, pa_dtype dt, const Grid& g, int8_t* x
 cudaError_t launch_attn_mma(const void* q, const void* k, const void* v, pa_dtype dt,
                             const Grid& g, const int32_t* idx, const int32_t* counts, int k_max,
                             void* out, int32_t* status, bool permuted, cudaStream_t s,
-                            const float* k_pool = nullptr, const float* v_pool = nullptr);
+                            const float* k_pool = nullptr, const float* v_pool = nullptr,
+                            float* lse = nullptr);
+cudaError_t launch_fill(float* x, float value, int64_t n, cudaStream_t s);
+// Rotary positions (rope.cu): make_rope_tab fills the table's layout and
+// returns its length in pairs
+int64_t make_rope_tab(const pa_rope& r, RopeTab* t);
+cudaError_t launch_rope_table(const RopeTab& t, double theta, const double* first,
+                              const double* step, float* table, cudaStream_t s);
+cudaError_t launch_rope(const void* x, RowStride xs, void* y, RowStride ys, pa_dtype dt,
+                        const Grid& g, const RopeTab& tab, bool interleaved, const float* table,
+                        const int32_t* positions, int64_t pos_batch, bool inverse,
+                        int32_t* status, cudaStream_t s);
+cudaError_t launch_rope_reorder(const void* x, RowStride xs, void* xp, pa_dtype dt, const Grid& g,
+                                const RopeTab& tab, bool interleaved, const float* table,
+                                float* pool, cudaStream_t s);
+// Single query tokens (query_attn.cu)
+cudaError_t launch_query_attn(const void* q, const void* k, const void* v, const float* k_pool,
+                              pa_dtype dt, const Grid& g, int group, int M, int k_keep,
+                              const int32_t* lengths, void* out, int32_t* idx, float* lse,
+                              int32_t* status, cudaStream_t s);
 // Selection variants (select_variants.cu)
 cudaError_t launch_sics(const void* x, pa_dtype dt, const Grid& g, float* scores, cudaStream_t s);
 cudaError_t launch_sics_pick(const float* scores, const Grid& g, int8_t* orders, cudaStream_t s);

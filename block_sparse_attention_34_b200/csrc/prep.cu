@@ -516,6 +516,20 @@ __global__ void round_bf16_kernel(const float* __restrict__ x, __nv_bfloat16* __
 }
 }  // namespace
 
+namespace {
+__global__ void fill_kernel(float* __restrict__ x, float value, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x)
+    x[i] = value;
+}
+}  // namespace
+
+cudaError_t launch_fill(float* x, float value, int64_t n, cudaStream_t s) {
+  const int64_t blocks = (n + 255) / 256;
+  fill_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(x, value, n);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_round_bf16(const float* x, void* y, int64_t n, cudaStream_t s) {
   const int64_t threads = (n + 7) / 8;
   const unsigned blocks = (unsigned)((threads + 255) / 256);

@@ -8,6 +8,7 @@ fails, an exception is raised.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -22,6 +23,7 @@ ABI_VERSION = 8  # the pa_abi_version() these signatures describe
 PA_F32, PA_BF16, PA_I8 = 0, 1, 2
 PA_ATTN_PERMUTED = 1
 PA_ATTN_P4 = 2  # with int8 inputs: 4-bit P codes (INT4 PV)
+PA_ROPE_INVERSE = 1  # pa_rope_apply: the transposed rotation
 PA_ATTN_P_TILE = 4  # with int8 inputs: normalised P, one scale per tile (two passes)
 STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_CUDA",
                 4: "PA_ERR_TIMEOUT", 5: "PA_ERR_DEVICE_CHECK"}
@@ -36,6 +38,11 @@ N_ORDERS = 12
 
 class PaShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "heads", "F", "H", "W", "d", "block")]
+
+
+class PaRope(ctypes.Structure):
+    _fields_ = [("extent", ctypes.c_int32 * 3), ("pairs", ctypes.c_int32 * 3),
+                ("interleaved", ctypes.c_int32)]
 
 
 class ParoError(RuntimeError):
@@ -87,6 +94,17 @@ def load():
         "pa_block_sparse_attn_compensated": ([_P, _P, _P, _I, ctypes.c_uint32, PaShape, _P, _P, _P, _I,
                                               _P, _P, _I, _P, _P, _P], _I),
         "pa_round_bf16": ([_P, _P, ctypes.c_int64, _P], _I),
+        "pa_rope_table_floats": ([PaRope], ctypes.c_int64),
+        "pa_rope_table": ([PaRope, ctypes.c_double, _P, _P, _P, _P], _I),
+        "pa_rope_apply": ([_P, _P, _P, _P, _I, PaShape, PaRope, _P, _P, _I, ctypes.c_uint32, _P,
+                           _P], _I),
+        "pa_rope_reorder": ([_P, _P, _P, _I, PaShape, _P, PaRope, _P, _P, _P], _I),
+        "pa_block_sparse_attn_lse": ([_P, _P, _P, _I, ctypes.c_uint32, PaShape, _P, _P, _P, _I, _P,
+                                      _P, _P, _P], _I),
+        "pa_block_sparse_attn_backward_workspace": ([PaShape], ctypes.c_int64),
+        "pa_block_sparse_attn_backward": ([_P] * 7 + [_I, PaShape, _P, _P, _P, _I, _P, _P, _P, _P,
+                                                      ctypes.c_int64, _P, _P], _I),
+        "pa_query_attn": ([_P, _P, _P, _P, _I, PaShape, _I, _I, _I, _P, _P, _P, _P, _P, _P], _I),
     }
     lib.pa_abi_version.restype = _I
     if lib.pa_abi_version() != ABI_VERSION:
@@ -529,6 +547,260 @@ def round_bf16(x, out=None):
         raise ValueError(f"out must be a contiguous bfloat16 tensor of shape {tuple(x.shape)}")
     _check(load().pa_round_bf16(_ptr(x), _ptr(out), x.numel(), _stream()))
     return out
+
+
+def _on(t):
+    """The device of ``t`` as the current one (its current stream is used)."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+class RopeTable:
+    """Rotary positions with three axes (time, height, width): the cosines
+    and sines of every coordinate of ``extent`` = (frames, height, width),
+    made once on the device and kept by the caller.
+
+    ``pairs``: how many of the head dimension's d/2 pairs turn with each axis,
+    in that order (the rest stay); default: a third of them each to height
+    and width, the rest to time.  Pair i of axis a turns by
+    ``(first[a] + step[a] * position) * theta ** (-i / pairs[a])``; ``first``
+    places a clip that continues another one, ``step`` stretches an axis.
+    ``interleaved``: pair p is elements (2p, 2p + 1), else (p, p + d/2)."""
+
+    def __init__(self, extent, d, pairs=None, theta=10000.0, first=(0.0, 0.0, 0.0),
+                 step=(1.0, 1.0, 1.0), interleaved=True, device="cuda"):
+        self.extent = tuple(int(x) for x in extent)
+        self.d = int(d)
+        if pairs is None:
+            third = self.d // 6
+            pairs = (self.d // 2 - 2 * third, third, third)
+        self.pairs = tuple(int(x) for x in pairs)
+        self.interleaved = bool(interleaved)
+        if not len(self.extent) == len(self.pairs) == len(first) == len(step) == 3:
+            raise ValueError("extent, pairs, first and step have one value per axis (3)")
+        if any(not 1 <= x < 1 << 31 for x in self.extent) or any(not 0 <= x <= 64 for x in self.pairs):
+            raise ValueError(f"extent {self.extent}, pairs {self.pairs}: extents >= 1, pairs 0 .. 64")
+        self.desc = PaRope((ctypes.c_int32 * 3)(*self.extent), (ctypes.c_int32 * 3)(*self.pairs),
+                           int(self.interleaved))
+        lib = load()
+        n = lib.pa_rope_table_floats(self.desc)
+        if n < 0 or sum(self.pairs) > self.d // 2:
+            raise ValueError(f"extent {self.extent}, pairs {self.pairs}: malformed for d = {self.d}")
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device (no CPU path)")
+        self.table = torch.empty(n, dtype=torch.float32, device=dev)
+        three = ctypes.c_double * 3
+        with _on(self.table):
+            _check(lib.pa_rope_table(self.desc, float(theta), three(*map(float, first)),
+                                     three(*map(float, step)), _ptr(self.table), _stream()))
+
+
+def _row_strides(t, name):
+    """Element strides (batch, head, token) of a [B, heads, N, d] tensor with
+    contiguous rows, as the library takes them."""
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    e = 16 // t.element_size()
+    # the stride of a dimension of one element says nothing
+    s = [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]
+    if any(x % e for x in s) or t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must start at multiples of 16 bytes (strides {t.stride()})")
+    return (ctypes.c_int64 * 3)(*s)
+
+
+def _rope_checks(x, rope, d):
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a CUDA device (no CPU path)")
+    if x.dim() != 4 or x.dtype not in _FLOAT:
+        raise ValueError(f"x: [B, heads, N, d] of float32 or bfloat16, got {tuple(x.shape)} {x.dtype}")
+    if rope.d != d or rope.table.device != x.device:
+        raise ValueError(f"rope: a table for d = {rope.d} on {rope.table.device}, x has d = {d} "
+                         f"on {x.device}")
+
+
+def _dense_rows(t):
+    """Whether no two elements of ``t`` share memory (dimensions sorted by
+    stride each step over the whole of the smaller ones)."""
+    at = 1
+    for stride, n in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):
+        if stride < at:
+            return False
+        at = stride * (n - 1) + at
+    return True
+
+
+def rope3d(x, rope: RopeTable, positions=None, inverse=False, out=None, status=None):
+    """Rotary positions with three axes of x [B, heads, N, d].
+
+    Rows must be contiguous and start at multiples of 16 bytes; batch, head
+    and token strides are free, so the projection's [B, N, heads, d] goes in
+    as ``.transpose(1, 2)``.  Token n sits at its place in the table's grid
+    (N = frames * height * width of ``rope.extent``), or at ``positions``
+    (int32 [N, 3] or [B, N, 3], contiguous; a coordinate outside the table is
+    reported on ``status`` and its rows stay unwritten).  ``inverse`` turns
+    back: the gradient's rotation.  ``out``: any non-overlapping strides, or
+    x itself; contiguous by default."""
+    _rope_checks(x, rope, x.shape[-1])
+    B, heads, N, d = x.shape
+    _need_cuda(positions, status)
+    if positions is None:
+        F, H, W = rope.extent
+        if F * H * W != N:
+            raise ValueError(f"x has {N} tokens, the table's grid {rope.extent}: give positions")
+    else:
+        F, H, W = 1, 1, N
+        _expect(positions, "positions", (N, 3) if positions.dim() == 2 else (B, N, 3), torch.int32)
+    for name, t in (("positions", positions), ("status", status), ("out", out)):
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name}: on {t.device}, x is on {x.device}")
+    _expect_status(status)
+    if 0 in x.shape:
+        raise ValueError(f"x: empty shape {tuple(x.shape)}")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _expect(out, "out", x.shape, x.dtype)
+        if not _dense_rows(out):
+            raise ValueError("out: rows overlap")
+    shape = PaShape(B, heads, F, H, W, d, 64)
+    with _on(x):
+        _check(load().pa_rope_apply(_ptr(x), _row_strides(x, "x"), _ptr(out),
+                                    _row_strides(out, "out"), _dtype_code(x), shape, rope.desc,
+                                    _ptr(rope.table), _ptr(positions),
+                                    int(positions is not None and positions.dim() == 3),
+                                    PA_ROPE_INVERSE if inverse else 0, _ptr(status), _stream()))
+    return out
+
+
+def rope_reorder(x, rope: RopeTable, pr: Problem, out=None, pool=None, with_pool=False):
+    """:func:`rope3d` and :func:`reorder` in one pass: the permuted copy
+    [B, heads, N_p, d] of the rotated x and, with ``with_pool`` (or a given
+    ``pool``), the block means of the rotated rows (taken before they are
+    rounded): returns (x_perm, pool).  x as for :func:`rope3d`."""
+    _rope_checks(x, rope, pr.d)
+    _need_cuda(out, pool)
+    _expect(x, "x", pr.natural, _FLOAT)
+    _expect(out, "out", pr.permuted, x.dtype)
+    _expect(pool, "pool", pr.pooled, torch.float32)
+    for name, t in (("out", out), ("pool", pool)):
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name}: on {t.device}, x is on {x.device}")
+    if any(e < n for e, n in zip(rope.extent, (pr.F, pr.H, pr.W))):
+        raise ValueError(f"rope.extent {rope.extent} does not cover the grid {(pr.F, pr.H, pr.W)}")
+    out = out if out is not None else torch.empty(pr.permuted, dtype=x.dtype, device=x.device)
+    if with_pool and pool is None:
+        pool = torch.empty(pr.pooled, dtype=torch.float32, device=x.device)
+    with _on(x):
+        _check(load().pa_rope_reorder(_ptr(x), _row_strides(x, "x"), _ptr(out), _dtype_code(x),
+                                      pr.shape, pr.perms_ptr, rope.desc, _ptr(rope.table),
+                                      _ptr(pool), _stream()))
+    return (out, pool) if (with_pool or pool is not None) else out
+
+
+def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=None, status=None,
+                          permuted=True):
+    """:func:`block_sparse_attn` for bf16 q, k, v (by default the permuted
+    copies of :func:`reorder` or :func:`rope_reorder`), which also returns
+    the natural log-sum-exp of every row, [B, heads, N] float32 (-inf for a
+    row without kept blocks): the forward pass of training."""
+    _need_cuda(q, k, v, idx, counts, out, lse, status)
+    rows = pr.permuted if permuted else pr.natural
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _expect(t, name, rows, torch.bfloat16)
+    _check_lists(idx, counts, pr)
+    _expect(out, "out", pr.natural, torch.bfloat16)
+    _expect(lse, "lse", pr.natural[:3], torch.float32)
+    _expect_status(status)
+    out = out if out is not None else torch.empty(pr.natural, dtype=torch.bfloat16, device=q.device)
+    lse = lse if lse is not None else torch.empty(pr.natural[:3], dtype=torch.float32, device=q.device)
+    with _on(q):
+        _check(load().pa_block_sparse_attn_lse(
+            _ptr(q), _ptr(k), _ptr(v), PA_BF16, PA_ATTN_PERMUTED if permuted else 0, pr.shape,
+            pr.perms_ptr, _ptr(idx), _ptr(counts), int(idx.shape[-1]), _ptr(out), _ptr(lse),
+            _ptr(status), _stream()))
+    return out, lse
+
+
+def block_sparse_attn_backward(dout, q, k, v, out, lse, pr: Problem, idx, counts=None, dlse=None,
+                               dq=None, dk=None, dv=None, workspace=None, status=None):
+    """Gradients (dq, dk, dv) [B, heads, N, d] of :func:`block_sparse_attn_lse`
+    in natural token order.  q, k, v: the permuted copies of the forward
+    pass; dout, out natural order; ``dlse``: the gradient of lse, if it was
+    used.  The same bits on every run.  ``workspace``: a uint8 tensor of at
+    least :func:`backward_workspace` bytes that no call in flight uses (by
+    default allocated here)."""
+    _need_cuda(dout, q, k, v, out, lse, idx, counts, dlse, dq, dk, dv, workspace, status)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _expect(t, name, pr.permuted, torch.bfloat16)
+    for name, t in (("dout", dout), ("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
+        _expect(t, name, pr.natural, torch.bfloat16)
+    for name, t in (("lse", lse), ("dlse", dlse)):
+        _expect(t, name, pr.natural[:3], torch.float32)
+    _check_lists(idx, counts, pr)
+    _expect_status(status)
+    dq, dk, dv = (t if t is not None else torch.empty(pr.natural, dtype=torch.bfloat16, device=q.device)
+                  for t in (dq, dk, dv))
+    if workspace is None:
+        workspace = torch.empty(backward_workspace(pr), dtype=torch.uint8, device=q.device)
+    elif workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace: dtype {workspace.dtype}, expected torch.uint8")
+    with _on(q):
+        _check(load().pa_block_sparse_attn_backward(
+            _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dlse), PA_BF16,
+            pr.shape, pr.perms_ptr, _ptr(idx), _ptr(counts), int(idx.shape[-1]), _ptr(dq),
+            _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _ptr(status), _stream()))
+    return dq, dk, dv
+
+
+def backward_workspace(pr: Problem) -> int:
+    """Bytes of workspace of :func:`block_sparse_attn_backward`."""
+    n = load().pa_block_sparse_attn_backward_workspace(pr.shape)
+    if n < 0:
+        raise ParoError(PA_ERR_UNSUPPORTED, load().pa_last_error().decode())
+    return n
+
+
+def block_sparse_query_attn(q, k, v, k_pool, pr: Problem, k_keep: int, lengths=None, out=None,
+                            idx=None, lse=None, status=None):
+    """Single query tokens against a stored clip (serving): every row of q
+    [B, q_heads, M, d] keeps the ``k_keep`` blocks with the largest
+    q . k_pool, ties to the lower index, and attends to their tokens.
+
+    k, v [B, heads, N_p, d]: the clip in the permuted order, k_pool
+    [B, heads, NB, d] float32 its block means (:func:`reorder` or
+    :func:`rope_reorder` with ``with_pool``); q_heads a multiple of heads
+    (query head h reads key head h // (q_heads / heads)).  ``lengths`` [B]
+    int32: how many positions of the order exist so far (0 .. N).  float32 or
+    bfloat16.  Returns (out [B, q_heads, M, d], idx [B, q_heads, M, k_keep]
+    ascending with -1 behind the last, lse [B, q_heads, M]); a row without
+    keys gives zeros and -inf."""
+    _need_cuda(q, k, v, k_pool, lengths, out, idx, lse, status)
+    if q.dim() != 4 or q.shape[0] != pr.B or q.shape[1] % pr.heads or q.shape[3] != pr.d or 0 in q.shape:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected ({pr.B}, a multiple of {pr.heads}, M, {pr.d})")
+    _expect(q, "q", tuple(q.shape), _FLOAT)
+    for name, t in (("k", k), ("v", v)):
+        _expect(t, name, pr.permuted, q.dtype)
+    _expect(k_pool, "k_pool", pr.pooled, torch.float32)
+    _expect(lengths, "lengths", (pr.B,), torch.int32)
+    rows = tuple(q.shape[:3])
+    _expect(out, "out", tuple(q.shape), q.dtype)
+    _expect(idx, "idx", rows + (int(k_keep),), torch.int32)
+    _expect(lse, "lse", rows, torch.float32)
+    _expect_status(status)
+    if not 1 <= k_keep <= pr.NB:
+        raise ValueError(f"k_keep={k_keep} must be in [1, {pr.NB}]")
+    dev = q.device
+    out = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=dev)
+    idx = idx if idx is not None else torch.empty(rows + (int(k_keep),), dtype=torch.int32, device=dev)
+    lse = lse if lse is not None else torch.empty(rows, dtype=torch.float32, device=dev)
+    with _on(q):
+        _check(load().pa_query_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _dtype_code(q),
+                                    pr.shape, q.shape[1] // pr.heads, q.shape[2], int(k_keep),
+                                    _ptr(lengths), _ptr(out), _ptr(idx), _ptr(lse), _ptr(status),
+                                    _stream()))
+    return out, idx, lse
 
 
 def choose_orders_sics(q, k, grid, block):

@@ -27,7 +27,11 @@
  * (pa_map_row_stats, pa_map_block_stats, pa_paro_metric, pa_paro_choose) and
  * PASA's compensation of the unselected blocks
  * (pa_block_sparse_attn_compensated, with pa_round_bf16 for bf16 block
- * means); pa_clear_status resets the device status word, and
+ * means); rotary positions of q and k with three axes (pa_rope_*), applied
+ * alone or on the way into the head's order (pa_rope_reorder); training
+ * (pa_block_sparse_attn_lse, pa_block_sparse_attn_backward) and serving of
+ * single query tokens against a stored clip (pa_query_attn);
+ * pa_clear_status resets the device status word, and
  * pa_test_inject_v_stall is the host-set hook of the bounded-wait test.
  *
  * Conventions shared by every entry point
@@ -406,6 +410,125 @@ PA_API pa_status pa_block_sparse_attn_compensated(const void* q, const void* k, 
  * overlapping; n = 0 does nothing.  Not an operation of the pages: a
  * storage conversion, so that the attention kernel moves 2-byte means. */
 PA_API pa_status pa_round_bf16(const float* x, void* y, int64_t n, void* stream);
+
+/* ---- Rotary positions with three axes (time, height, width) ----------
+ *
+ * The d/2 pairs of a row are dealt to the axes in order: the first pairs[0]
+ * to time, the next pairs[1] to height, the next pairs[2] to width; the
+ * rest are not rotated.  Pair i of axis a turns by
+ *   angle = (first[a] + step[a] * pos_a) * theta^(-i / pairs[a]),
+ *   (y0, y1) = (x0 cos - x1 sin, x0 sin + x1 cos),
+ * where pos_a in [0, extent[a]) is the token's coordinate.  Pair p holds
+ * elements 2p and 2p+1 (interleaved = 1) or p and p + d/2 (interleaved = 0).
+ * first and step place a table's coordinates: first[0] = the frames already
+ * generated, step < 1 to interpolate. */
+typedef struct {
+  int32_t extent[3];
+  int32_t pairs[3];
+  int32_t interleaved;
+} pa_rope;
+
+/* Floats of the table of `rope`, or -1 if it is malformed (extents >= 1,
+ * pairs >= 0 with a sum of 1 .. 64, interleaved 0 or 1, at most 2^31
+ * floats).  An axis without pairs has no table rows. */
+PA_API int64_t pa_rope_table_floats(pa_rope rope);
+
+/* Fill the table (pa_rope_table_floats floats, device memory, 16-byte
+ * aligned): the cosines and sines of every coordinate of every axis, their
+ * angles computed in 64 bits and each value rounded once to a float.
+ * theta > 0, first and step finite. */
+PA_API pa_status pa_rope_table(pa_rope rope, double theta, const double first[3],
+                               const double step[3], float* table, void* stream);
+
+/* The rotation: x -> y, both [B, heads, N, d] (PA_F32 or PA_BF16) with
+ * contiguous rows and element strides x_stride, y_stride of batch, head and
+ * token (HOST memory, 3 each; NULL: contiguous).  Bases 16-byte aligned,
+ * strides >= 0 and multiples of 16 bytes (an x stride may be 0, a y tensor's
+ * rows must not overlap).  y == x with equal strides rotates in place.
+ * positions: NULL for token n at (n / (H W), n / W % H, n % W) of the grid
+ * shape.F x H x W, which extent must then cover; or int32 [N, 3] device
+ * memory (positions_batched = 0, every batch element alike) or [B, N, 3]
+ * (positions_batched = 1); a token with a coordinate outside [0, extent) is
+ * reported on dev_status (PA_ERR_DEVICE_CHECK) and its rows are left
+ * unwritten.  flags: PA_ROPE_INVERSE for the transposed rotation (angle
+ * negated), which takes y's gradient to x's.  sum of pairs <= d/2;
+ * B <= 65535.  shape.block is not used. */
+#define PA_ROPE_INVERSE 1u
+PA_API pa_status pa_rope_apply(const void* x, const int64_t* x_stride, void* y,
+                               const int64_t* y_stride, pa_dtype dtype, pa_shape shape,
+                               pa_rope rope, const float* table, const int32_t* positions,
+                               int32_t positions_batched, uint32_t flags, int32_t* dev_status,
+                               void* stream);
+
+/* pa_rope_apply (grid positions) and pa_reorder in one pass: x [B, heads,
+ * N, d] with strides as above -> the permuted copy x_perm [B,heads,N_p,d]
+ * of the rotated rows, pad rows zero; pool, if not NULL, [B,heads,NB,d]
+ * float, receives the mean of each block's valid rotated rows (before they
+ * are rounded to dtype).  B * heads <= 65535. */
+PA_API pa_status pa_rope_reorder(const void* x, const int64_t* x_stride, void* x_perm,
+                                 pa_dtype dtype, pa_shape shape, const int8_t* perms,
+                                 pa_rope rope, const float* table, float* pool, void* stream);
+
+/* ---- Training ---------------------------------------------------------
+ *
+ * pa_block_sparse_attn for dtype PA_BF16 (PA_ERR_UNSUPPORTED otherwise),
+ * which also stores lse[b,h,n] = log sum_c exp(q_n . k_c / sqrt(d)) over
+ * the row's kept keys (natural log; [B,heads,N] float, natural order; -inf
+ * for a row without kept blocks).  out is the same, bit for bit. */
+PA_API pa_status pa_block_sparse_attn_lse(const void* q, const void* k, const void* v,
+                                          pa_dtype dtype, uint32_t flags, pa_shape shape,
+                                          const int8_t* perms, const int32_t* idx,
+                                          const int32_t* counts, int32_t k_max, void* out,
+                                          float* lse, int32_t* dev_status, void* stream);
+
+/* Bytes of workspace of pa_block_sparse_attn_backward, or -1 for a shape it
+ * does not take. */
+PA_API int64_t pa_block_sparse_attn_backward_workspace(pa_shape shape);
+
+/* Gradients of pa_block_sparse_attn_lse (PA_BF16): with P = exp(S - lse) on
+ * the kept tiles, D_n = dout_n . out_n - dlse_n, dS = P o (dout V^T - D),
+ *   dq = dS K / sqrt(d),  dk = dS^T Q / sqrt(d),  dv = P^T dout.
+ * q, k, v: the permuted copies [B,heads,N_p,d] that the forward pass took
+ * with PA_ATTN_PERMUTED (pa_reorder's output, pad rows zero); dout, out, dq,
+ * dk, dv [B,heads,N,d] bf16 natural order; lse, dlse (may be NULL: zero)
+ * [B,heads,N] float.  idx, counts, k_max as in the forward pass; the
+ * selection itself is not differentiated.  P and dS are rounded to bf16 for
+ * their products; every sum is fp32, in the same order on every run.  Rows
+ * without kept blocks get dq = 0, keys that no row keeps dk = dv = 0.  A
+ * malformed list is reported on dev_status (PA_ERR_DEVICE_CHECK): its rows
+ * of dq are left unwritten and it adds nothing to dk and dv.
+ * workspace: pa_block_sparse_attn_backward_workspace bytes, device memory,
+ * 256-byte aligned, used by this call alone until it completes.
+ * NB <= 65535, B * heads <= 65535. */
+PA_API pa_status pa_block_sparse_attn_backward(
+    const void* dout, const void* q, const void* k, const void* v, const void* out,
+    const float* lse, const float* dlse, pa_dtype dtype, pa_shape shape, const int8_t* perms,
+    const int32_t* idx, const int32_t* counts, int32_t k_max, void* dq, void* dk, void* dv,
+    void* workspace, int64_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* ---- Serving: single query tokens against a stored clip ---------------
+ *
+ * Query row m of head hq (key head hq / q_group): block scores q . k_pool_j
+ * (summed in 64 bits; NaN read as -inf), the k_keep blocks with the largest
+ * (ties to the lower index), softmax attention over their tokens:
+ *   out[b,hq,m,:] = sum_c softmax_c(q . k_c / sqrt(d)) v_c.
+ * q, out [B, heads*q_group, M, d]; k, v [B,heads,N_p,d] in the permuted
+ * order; k_pool [B,heads,NB,d] float, the blocks' mean keys; dtype PA_F32 or
+ * PA_BF16, every product and sum in at least fp32.  lengths: NULL, or [B]
+ * int32 device memory in [0, N]: only the first lengths[b] positions of the
+ * order exist, blocks at or past them are no candidates and rows behind them
+ * are never used (their k and v may hold anything); another value is
+ * reported on dev_status (PA_ERR_DEVICE_CHECK) and its rows are left
+ * unwritten.  idx [B,heads*q_group,M,k_keep] int32: the kept blocks,
+ * ascending, -1 behind the last where fewer exist.  lse (may be NULL)
+ * [B,heads*q_group,M] float: natural log-sum-exp of the row.  A row without
+ * keys gives zeros and lse -inf.  1 <= k_keep <= NB <= 14528; M, q_group
+ * >= 1; B*heads*q_group*M <= 2^27.  perms are not needed: shape's order is
+ * the caller's. */
+PA_API pa_status pa_query_attn(const void* q, const void* k, const void* v, const float* k_pool,
+                               pa_dtype dtype, pa_shape shape, int32_t q_group, int32_t M,
+                               int32_t k_keep, const int32_t* lengths, void* out, int32_t* idx,
+                               float* lse, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }
