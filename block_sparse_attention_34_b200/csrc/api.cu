@@ -652,7 +652,7 @@ namespace {
 // The backward pass's workspace: dO permuted, row statistics, transposed
 // kept lists, each at a multiple of 256 bytes.
 struct BwdLayout {
-  int64_t stats, mask, bytes;
+  int64_t nlse, ndel, mask, bytes;
   int words;
 };
 BwdLayout bwd_layout(const paro::Grid& g) {
@@ -660,8 +660,9 @@ BwdLayout bwd_layout(const paro::Grid& g) {
   const int64_t rows = (int64_t)g.B * g.heads * g.Np;
   BwdLayout l;
   l.words = (g.NB + 31) / 32;
-  l.stats = up(rows * g.d * 2);
-  l.mask = l.stats + up(rows * 8);
+  l.nlse = up(rows * g.d * 2);
+  l.ndel = l.nlse + up(rows * 4);
+  l.mask = l.ndel + up(rows * 4);
   l.bytes = l.mask + up((int64_t)g.B * g.heads * g.NB * l.words * 4);
   return l;
 }
@@ -710,7 +711,8 @@ pa_status pa_block_sparse_attn_backward(const void* dout, const void* q, const v
   a.k = static_cast<const __nv_bfloat16*>(k);
   a.v = static_cast<const __nv_bfloat16*>(v);
   a.dop = reinterpret_cast<__nv_bfloat16*>(w);
-  a.stats = reinterpret_cast<float2*>(w + l.stats);
+  a.nlse = reinterpret_cast<float*>(w + l.nlse);
+  a.ndel = reinterpret_cast<float*>(w + l.ndel);
   a.mask = reinterpret_cast<uint32_t*>(w + l.mask);
   a.words = l.words;
   a.idx = idx;
@@ -722,7 +724,8 @@ pa_status pa_block_sparse_attn_backward(const void* dout, const void* q, const v
   a.status = dev_status;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = paro::launch_bwd_prep(out, dout, lse, dlse, a, g, s);
-  if (e == cudaSuccess) e = paro::launch_bwd_mma(a, g, s);
+  if (e == cudaSuccess)
+    e = paro::bwd_sm100_supports(g) ? paro::launch_bwd_sm100(a, g, s) : paro::launch_bwd_mma(a, g, s);
   return cuda_status(e, "pa_block_sparse_attn_backward launch");
 }
 

@@ -14,8 +14,8 @@
 // twice (7 products a tile instead of 5; an fp32 dQ of 64 KB a tile added
 // through L2 would cost about as much as the two products).
 //
-// Preparation: dO is copied to the permuted order with each row's (lse in
-// log2 units, D) beside it, pad rows as (inf, 0) so that they drop out of
+// Preparation: dO is copied to the permuted order with each row's -lse (log2
+// units) and -D beside it, pad rows as (-inf, 0) so that they drop out of
 // every sum as P = 0; the kept lists are transposed to one bit per (key
 // block, query block).
 #include "bwd.cuh"
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads)
     bwd_prep_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
                     const float* __restrict__ lse, const float* __restrict__ dlse,
                     const __grid_constant__ Grid g, __nv_bfloat16* __restrict__ dop,
-                    float2* __restrict__ stats) {
+                    float* __restrict__ nlse, float* __restrict__ ndel) {
   constexpr int VPR = D / 8;
   const int c = threadIdx.x % VPR;
   const int64_t bh = blockIdx.y;
@@ -58,12 +58,8 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t prow = bh * g.Np + p;
   reinterpret_cast<uint4*>(dop + prow * D)[c] = d;
   if (c == 0) {
-    float2 st = make_float2(INFINITY, 0.f);
-    if (row >= 0) {
-      st.x = __ldg(lse + row) * kLog2e;
-      st.y = s - (dlse != nullptr ? __ldg(dlse + row) : 0.f);
-    }
-    stats[prow] = st;
+    nlse[prow] = row >= 0 ? -__ldg(lse + row) * kLog2e : -INFINITY;
+    ndel[prow] = row >= 0 ? (dlse != nullptr ? __ldg(dlse + row) : 0.f) - s : 0.f;
   }
 }
 
@@ -138,7 +134,7 @@ template <int D, int BLOCK, bool kKeys>
 __global__ void __launch_bounds__(BLOCK * 2)
     bwd_mma_kernel(const __nv_bfloat16* __restrict__ a1, const __nv_bfloat16* __restrict__ a2,
                    const __nv_bfloat16* __restrict__ b1, const __nv_bfloat16* __restrict__ b2,
-                   const float2* __restrict__ stats, const __grid_constant__ Grid g,
+                   const float* __restrict__ nlse, const float* __restrict__ ndel, const __grid_constant__ Grid g,
                    const int32_t* __restrict__ idx, const int32_t* __restrict__ counts, int k_max,
                    const uint32_t* __restrict__ mask, int words, float scale,
                    __nv_bfloat16* __restrict__ g1, __nv_bfloat16* __restrict__ g2,
@@ -151,7 +147,7 @@ __global__ void __launch_bounds__(BLOCK * 2)
   __nv_bfloat16* A2 = A1 + kTileElems;
   __nv_bfloat16* B1 = A2 + kTileElems;
   __nv_bfloat16* B2 = B1 + kTileElems;
-  float2* st = reinterpret_cast<float2*>(B2 + kTileElems);  // the query rows' statistics
+  float2* st = reinterpret_cast<float2*>(B2 + kTileElems);  // the query rows' (-lse, -D)
 
   const int t = blockIdx.x;  // this CTA's block
   const int64_t bh = blockIdx.y;
@@ -177,9 +173,9 @@ __global__ void __launch_bounds__(BLOCK * 2)
   if constexpr (!kKeys) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float2 s = __ldg(stats + head + t * BLOCK + warp * 16 + lane / 4 + 8 * u);
-      lse_r[u] = s.x;
-      d_r[u] = s.y;
+      const int64_t at = head + t * BLOCK + warp * 16 + lane / 4 + 8 * u;
+      lse_r[u] = __ldg(nlse + at);
+      d_r[u] = __ldg(ndel + at);
     }
   }
   float acc1[DT][4], acc2[kKeys ? DT : 1][4];
@@ -197,7 +193,8 @@ __global__ void __launch_bounds__(BLOCK * 2)
     load_tile<D, LD, BLOCK>(B2, b2 + (head + (int64_t)j * BLOCK) * D);
     if constexpr (kKeys)
       for (int e = threadIdx.x; e < BLOCK; e += blockDim.x)
-        st[e] = __ldg(stats + head + (int64_t)j * BLOCK + e);
+        st[e] = make_float2(__ldg(nlse + head + (int64_t)j * BLOCK + e),
+                            __ldg(ndel + head + (int64_t)j * BLOCK + e));
     __syncthreads();
 #pragma unroll 1
     for (int c0 = 0; c0 < BLOCK; c0 += 32) {
@@ -243,11 +240,11 @@ __global__ void __launch_bounds__(BLOCK * 2)
             l = lse_r[e >> 1];
             dd = d_r[e >> 1];
           }
-          float p = exp2f(fmaf(x[nt][e], scale_log2, -l));
+          float p = exp2f(fmaf(x[nt][e], scale_log2, l));
           if constexpr (!kKeys)
             if (j * BLOCK + col >= g.N) p = 0.f;  // pad keys
           x[nt][e] = p;
-          y[nt][e] = p * (y[nt][e] - dd);
+          y[nt][e] = p * (y[nt][e] + dd);
         }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
@@ -319,9 +316,9 @@ cudaError_t launch_mma(const BwdArgs& a, const Grid& g, cudaStream_t s) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kv<<<grid, BLOCK * 2, smem, s>>>(a.k, a.v, a.q, a.dop, a.stats, g, nullptr, nullptr, 0, a.mask,
+  kv<<<grid, BLOCK * 2, smem, s>>>(a.k, a.v, a.q, a.dop, a.nlse, a.ndel, g, nullptr, nullptr, 0, a.mask,
                                    a.words, scale, a.dk, a.dv, a.status);
-  kq<<<grid, BLOCK * 2, smem, s>>>(a.q, a.dop, a.k, a.v, a.stats, g, a.idx, a.counts, a.k_max,
+  kq<<<grid, BLOCK * 2, smem, s>>>(a.q, a.dop, a.k, a.v, a.nlse, a.ndel, g, a.idx, a.counts, a.k_max,
                                    nullptr, 0, scale, a.dq, nullptr, a.status);
   return cudaGetLastError();
 }
@@ -341,9 +338,9 @@ cudaError_t launch_bwd_prep(const void* out, const void* dout, const float* lse,
   auto* o = static_cast<const __nv_bfloat16*>(out);
   auto* d = static_cast<const __nv_bfloat16*>(dout);
   if (g.d == 64)
-    bwd_prep_kernel<64><<<grid, kThreads, 0, s>>>(o, d, lse, dlse, g, a.dop, a.stats);
+    bwd_prep_kernel<64><<<grid, kThreads, 0, s>>>(o, d, lse, dlse, g, a.dop, a.nlse, a.ndel);
   else
-    bwd_prep_kernel<128><<<grid, kThreads, 0, s>>>(o, d, lse, dlse, g, a.dop, a.stats);
+    bwd_prep_kernel<128><<<grid, kThreads, 0, s>>>(o, d, lse, dlse, g, a.dop, a.nlse, a.ndel);
   return cudaGetLastError();
 }
 

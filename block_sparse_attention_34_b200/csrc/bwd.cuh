@@ -9,7 +9,7 @@ namespace paro {
 struct BwdArgs {
   const __nv_bfloat16 *q, *k, *v;  // permuted [B*heads, Np, d]
   __nv_bfloat16* dop;              // workspace: dO in the permuted order
-  float2* stats;                   // workspace: (lse log2 e, D) of each permuted row
+  float *nlse, *ndel;              // workspace: -lse log2 e and -D of each permuted row
   uint32_t* mask;                  // workspace: [B*heads, NB, words], bit i of row j: i keeps j
   int words;
   const int32_t *idx, *counts;
@@ -34,6 +34,10 @@ __device__ __forceinline__ bool list_ok(const int32_t* __restrict__ ids, int cnt
 
 cudaError_t launch_bwd_prep(const void* out, const void* dout, const float* lse,
                             const float* dlse, const BwdArgs& a, const Grid& g, cudaStream_t s);
+// The tensor-core kernels of block 128 (attn_bwd_sm100.cu), the warp-level
+// ones of every shape (attn_bwd.cu).
+bool bwd_sm100_supports(const Grid& g);
+cudaError_t launch_bwd_sm100(const BwdArgs& a, const Grid& g, cudaStream_t s);
 cudaError_t launch_bwd_mma(const BwdArgs& a, const Grid& g, cudaStream_t s);
 
 }  // namespace paro
