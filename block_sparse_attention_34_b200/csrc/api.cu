@@ -514,7 +514,7 @@ static const char* rope_fault(const pa_rope& r) {
 int64_t pa_rope_table_floats(pa_rope rope) {
   if (rope_fault(rope) != nullptr) return -1;
   paro::RopeTab tab;
-  return 2 * paro::make_rope_tab(rope, &tab);
+  return paro::make_rope_tab(rope, &tab);
 }
 
 pa_status pa_rope_table(pa_rope rope, double theta, const double first[3], const double step[3],

@@ -41,12 +41,14 @@ struct Grid {
   int8_t perm[kMaxHeads];
 };
 
-// Rotary positions (rope.cu): for each axis its table rows, its pairs, its
-// first pair, the groups of four pairs of a table row, and where its rows
-// start (in pairs).
+// Rotary positions (rope.cu): for each axis (the fourth: the pairs that
+// stay) its table rows, its pairs, its first pair, the groups of four pairs
+// of a table row, and where its rows start (in floats); tiny: some group of
+// four holds pairs of three axes.
 struct RopeTab {
-  int32_t extent[3], pairs[3], start[3], groups[3];
-  int64_t offset[3];
+  int32_t extent[4], pairs[4], start[4], groups[4];
+  int64_t offset[4];
+  int32_t tiny;
 };
 // Element strides of a [B, heads, N, d] tensor whose rows are contiguous.
 struct RowStride {
@@ -172,7 +174,7 @@ cudaError_t launch_attn_mma(const void* q, const void* k, const void* v, pa_dtyp
                             float* lse = nullptr);
 cudaError_t launch_fill(float* x, float value, int64_t n, cudaStream_t s);
 // Rotary positions (rope.cu): make_rope_tab fills the table's layout and
-// returns its length in pairs
+// returns its length in floats
 int64_t make_rope_tab(const pa_rope& r, RopeTab* t);
 cudaError_t launch_rope_table(const RopeTab& t, double theta, const double* first,
                               const double* step, float* table, cudaStream_t s);

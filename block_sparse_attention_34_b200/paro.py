@@ -8,8 +8,8 @@ fails, an exception is raised.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -194,6 +194,7 @@ class Problem:
             raise ValueError(f"perms must have one order id per head ({self.heads})")
         self._perms = np.ascontiguousarray(p)
         self.shape = PaShape(self.B, self.heads, self.F, self.H, self.W, self.d, self.block)
+        self.perms_ptr = self._perms.ctypes.data_as(ctypes.c_void_p)
 
     @property
     def natural(self):
@@ -214,10 +215,6 @@ class Problem:
     @property
     def per_block(self):
         return (self.B, self.heads, self.NB)
-
-    @property
-    def perms_ptr(self):
-        return self._perms.ctypes.data_as(ctypes.c_void_p)
 
     @classmethod
     def from_qkv(cls, q, grid, perms, block):
@@ -549,11 +546,44 @@ def round_bf16(x, out=None):
     return out
 
 
-def _on(t):
-    """The device of ``t`` as the current one (its current stream is used)."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+def _launch(t, fn, *args):
+    """fn(*args, stream) on the device of ``t`` and its current stream."""
+    i = t.get_device()
+    if i == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, _raw_stream(i))
+    if status != PA_OK:
+        raise ParoError(status, load().pa_last_error().decode())
+
+
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _same_device(t, *named):
+    """Raise ValueError unless the tensors given are contiguous and on the
+    device of ``t``."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("tensors must be on a CUDA device (no CPU path)")
+    for name, u in named:
+        if u is None:
+            continue
+        if u.get_device() != i:
+            raise ValueError(f"{name}: on {u.device}, expected {t.device}")
+        if not u.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _row_shape(B, heads, F, H, W, d):
+    return PaShape(B, heads, F, H, W, d, 64)
 
 
 class RopeTable:
@@ -592,15 +622,16 @@ class RopeTable:
             raise ValueError("tensors must be on a CUDA device (no CPU path)")
         self.table = torch.empty(n, dtype=torch.float32, device=dev)
         three = ctypes.c_double * 3
-        with _on(self.table):
-            _check(lib.pa_rope_table(self.desc, float(theta), three(*map(float, first)),
-                                     three(*map(float, step)), _ptr(self.table), _stream()))
+        _launch(self.table, lib.pa_rope_table, self.desc, float(theta), three(*map(float, first)),
+                three(*map(float, step)), _addr(self.table))
 
 
 def _row_strides(t, name):
     """Element strides (batch, head, token) of a [B, heads, N, d] tensor with
-    contiguous rows, as the library takes them."""
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    contiguous rows, as the library takes them (None: contiguous)."""
+    if t.data_ptr() % 16 == 0 and t.is_contiguous():
+        return None
+    if t.stride(3) != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     e = 16 // t.element_size()
     # the stride of a dimension of one element says nothing
@@ -611,12 +642,12 @@ def _row_strides(t, name):
 
 
 def _rope_checks(x, rope, d):
-    if not x.is_cuda:
+    if x.get_device() < 0:
         raise ValueError("tensors must be on a CUDA device (no CPU path)")
-    if x.dim() != 4 or x.dtype not in _FLOAT:
+    if x.dim() != 4 or x.dtype not in _FLOAT or x.numel() == 0:
         raise ValueError(f"x: [B, heads, N, d] of float32 or bfloat16, got {tuple(x.shape)} {x.dtype}")
-    if rope.d != d or rope.table.device != x.device:
-        raise ValueError(f"rope: a table for d = {rope.d} on {rope.table.device}, x has d = {d} "
+    if rope.d != d or x.shape[3] != d or rope.table.get_device() != x.get_device():
+        raise ValueError(f"rope: a table for d = {rope.d} on {rope.table.device}, x has d = {x.shape[3]} "
                          f"on {x.device}")
 
 
@@ -641,36 +672,36 @@ def rope3d(x, rope: RopeTable, positions=None, inverse=False, out=None, status=N
     (int32 [N, 3] or [B, N, 3], contiguous; a coordinate outside the table is
     reported on ``status`` and its rows stay unwritten).  ``inverse`` turns
     back: the gradient's rotation.  ``out``: any non-overlapping strides, or
-    x itself; contiguous by default."""
-    _rope_checks(x, rope, x.shape[-1])
+    x itself (not a tensor that shares only part of x's memory); contiguous
+    by default."""
+    _rope_checks(x, rope, rope.d)
+    _same_device(x, ("positions", positions), ("status", status))
     B, heads, N, d = x.shape
-    _need_cuda(positions, status)
     if positions is None:
         F, H, W = rope.extent
         if F * H * W != N:
             raise ValueError(f"x has {N} tokens, the table's grid {rope.extent}: give positions")
+        batched = 0
     else:
         F, H, W = 1, 1, N
-        _expect(positions, "positions", (N, 3) if positions.dim() == 2 else (B, N, 3), torch.int32)
-    for name, t in (("positions", positions), ("status", status), ("out", out)):
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name}: on {t.device}, x is on {x.device}")
+        batched = int(positions.dim() == 3)
+        if positions.shape != ((B, N, 3) if batched else (N, 3)) or positions.dtype != torch.int32:
+            raise ValueError(f"positions: {tuple(positions.shape)} {positions.dtype}, expected int32 "
+                             f"({N}, 3) or ({B}, {N}, 3)")
     _expect_status(status)
-    if 0 in x.shape:
-        raise ValueError(f"x: empty shape {tuple(x.shape)}")
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out_strides = None
     else:
         _expect(out, "out", x.shape, x.dtype)
+        if out.get_device() != x.get_device():
+            raise ValueError(f"out: on {out.device}, x is on {x.device}")
         if not _dense_rows(out):
             raise ValueError("out: rows overlap")
-    shape = PaShape(B, heads, F, H, W, d, 64)
-    with _on(x):
-        _check(load().pa_rope_apply(_ptr(x), _row_strides(x, "x"), _ptr(out),
-                                    _row_strides(out, "out"), _dtype_code(x), shape, rope.desc,
-                                    _ptr(rope.table), _ptr(positions),
-                                    int(positions is not None and positions.dim() == 3),
-                                    PA_ROPE_INVERSE if inverse else 0, _ptr(status), _stream()))
+        out_strides = _row_strides(out, "out")
+    _launch(x, load().pa_rope_apply, x.data_ptr(), _row_strides(x, "x"), out.data_ptr(), out_strides,
+            _dtype_code(x), _row_shape(B, heads, F, H, W, d), rope.desc, rope.table.data_ptr(),
+            _addr(positions), batched, PA_ROPE_INVERSE if inverse else 0, _addr(status))
     return out
 
 
@@ -678,25 +709,29 @@ def rope_reorder(x, rope: RopeTable, pr: Problem, out=None, pool=None, with_pool
     """:func:`rope3d` and :func:`reorder` in one pass: the permuted copy
     [B, heads, N_p, d] of the rotated x and, with ``with_pool`` (or a given
     ``pool``), the block means of the rotated rows (taken before they are
-    rounded): returns (x_perm, pool).  x as for :func:`rope3d`."""
+    rounded): returns (x_perm, pool).  x as for :func:`rope3d`, token n at
+    its place in pr's grid, which ``rope.extent`` has to cover."""
     _rope_checks(x, rope, pr.d)
-    _need_cuda(out, pool)
-    _expect(x, "x", pr.natural, _FLOAT)
+    _same_device(x, ("out", out), ("pool", pool))
+    if x.shape != pr.natural:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected {pr.natural}")
+    if rope.extent[0] < pr.F or rope.extent[1] < pr.H or rope.extent[2] < pr.W:
+        raise ValueError(f"rope.extent {rope.extent} does not cover the grid {(pr.F, pr.H, pr.W)}")
     _expect(out, "out", pr.permuted, x.dtype)
     _expect(pool, "pool", pr.pooled, torch.float32)
-    for name, t in (("out", out), ("pool", pool)):
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name}: on {t.device}, x is on {x.device}")
-    if any(e < n for e, n in zip(rope.extent, (pr.F, pr.H, pr.W))):
-        raise ValueError(f"rope.extent {rope.extent} does not cover the grid {(pr.F, pr.H, pr.W)}")
-    out = out if out is not None else torch.empty(pr.permuted, dtype=x.dtype, device=x.device)
+    if out is None:
+        out = torch.empty(pr.permuted, dtype=x.dtype, device=x.device)
     if with_pool and pool is None:
         pool = torch.empty(pr.pooled, dtype=torch.float32, device=x.device)
-    with _on(x):
-        _check(load().pa_rope_reorder(_ptr(x), _row_strides(x, "x"), _ptr(out), _dtype_code(x),
-                                      pr.shape, pr.perms_ptr, rope.desc, _ptr(rope.table),
-                                      _ptr(pool), _stream()))
-    return (out, pool) if (with_pool or pool is not None) else out
+    _launch(x, load().pa_rope_reorder, x.data_ptr(), _row_strides(x, "x"), out.data_ptr(),
+            _dtype_code(x), pr.shape, pr.perms_ptr, rope.desc, rope.table.data_ptr(), _addr(pool))
+    return (out, pool) if pool is not None else out
+
+
+def _bf16(shape, *named):
+    for name, t in named:
+        if t is not None and (t.shape != shape or t.dtype != torch.bfloat16):
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} torch.bfloat16")
 
 
 def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=None, status=None,
@@ -705,21 +740,18 @@ def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=
     copies of :func:`reorder` or :func:`rope_reorder`), which also returns
     the natural log-sum-exp of every row, [B, heads, N] float32 (-inf for a
     row without kept blocks): the forward pass of training."""
-    _need_cuda(q, k, v, idx, counts, out, lse, status)
-    rows = pr.permuted if permuted else pr.natural
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _expect(t, name, rows, torch.bfloat16)
+    _same_device(q, ("q", q), ("k", k), ("v", v), ("idx", idx), ("counts", counts), ("out", out),
+                 ("lse", lse), ("status", status))
+    _bf16(pr.permuted if permuted else pr.natural, ("q", q), ("k", k), ("v", v))
     _check_lists(idx, counts, pr)
     _expect(out, "out", pr.natural, torch.bfloat16)
     _expect(lse, "lse", pr.natural[:3], torch.float32)
     _expect_status(status)
     out = out if out is not None else torch.empty(pr.natural, dtype=torch.bfloat16, device=q.device)
     lse = lse if lse is not None else torch.empty(pr.natural[:3], dtype=torch.float32, device=q.device)
-    with _on(q):
-        _check(load().pa_block_sparse_attn_lse(
-            _ptr(q), _ptr(k), _ptr(v), PA_BF16, PA_ATTN_PERMUTED if permuted else 0, pr.shape,
-            pr.perms_ptr, _ptr(idx), _ptr(counts), int(idx.shape[-1]), _ptr(out), _ptr(lse),
-            _ptr(status), _stream()))
+    _launch(q, load().pa_block_sparse_attn_lse, q.data_ptr(), k.data_ptr(), v.data_ptr(), PA_BF16,
+            PA_ATTN_PERMUTED if permuted else 0, pr.shape, pr.perms_ptr, _addr(idx), _addr(counts),
+            idx.shape[3], out.data_ptr(), lse.data_ptr(), _addr(status))
     return out, lse
 
 
@@ -731,26 +763,24 @@ def block_sparse_attn_backward(dout, q, k, v, out, lse, pr: Problem, idx, counts
     used.  The same bits on every run.  ``workspace``: a uint8 tensor of at
     least :func:`backward_workspace` bytes that no call in flight uses (by
     default allocated here)."""
-    _need_cuda(dout, q, k, v, out, lse, idx, counts, dlse, dq, dk, dv, workspace, status)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _expect(t, name, pr.permuted, torch.bfloat16)
-    for name, t in (("dout", dout), ("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
-        _expect(t, name, pr.natural, torch.bfloat16)
+    _same_device(q, ("q", q), ("k", k), ("v", v), ("dout", dout), ("out", out), ("lse", lse),
+                 ("idx", idx), ("counts", counts), ("dlse", dlse), ("dq", dq), ("dk", dk), ("dv", dv),
+                 ("workspace", workspace), ("status", status))
+    _bf16(pr.permuted, ("q", q), ("k", k), ("v", v))
+    _bf16(pr.natural, ("dout", dout), ("out", out), ("dq", dq), ("dk", dk), ("dv", dv))
     for name, t in (("lse", lse), ("dlse", dlse)):
         _expect(t, name, pr.natural[:3], torch.float32)
     _check_lists(idx, counts, pr)
     _expect_status(status)
-    dq, dk, dv = (t if t is not None else torch.empty(pr.natural, dtype=torch.bfloat16, device=q.device)
-                  for t in (dq, dk, dv))
+    dq, dk, dv = (t if t is not None else torch.empty_like(out) for t in (dq, dk, dv))
     if workspace is None:
         workspace = torch.empty(backward_workspace(pr), dtype=torch.uint8, device=q.device)
     elif workspace.dtype != torch.uint8:
         raise ValueError(f"workspace: dtype {workspace.dtype}, expected torch.uint8")
-    with _on(q):
-        _check(load().pa_block_sparse_attn_backward(
-            _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dlse), PA_BF16,
-            pr.shape, pr.perms_ptr, _ptr(idx), _ptr(counts), int(idx.shape[-1]), _ptr(dq),
-            _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _ptr(status), _stream()))
+    _launch(q, load().pa_block_sparse_attn_backward, dout.data_ptr(), q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), out.data_ptr(), lse.data_ptr(), _addr(dlse), PA_BF16, pr.shape,
+            pr.perms_ptr, _addr(idx), _addr(counts), idx.shape[3], dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr(), workspace.data_ptr(), workspace.numel(), _addr(status))
     return dq, dk, dv
 
 
@@ -776,16 +806,20 @@ def block_sparse_query_attn(q, k, v, k_pool, pr: Problem, k_keep: int, lengths=N
     bfloat16.  Returns (out [B, q_heads, M, d], idx [B, q_heads, M, k_keep]
     ascending with -1 behind the last, lse [B, q_heads, M]); a row without
     keys gives zeros and -inf."""
-    _need_cuda(q, k, v, k_pool, lengths, out, idx, lse, status)
-    if q.dim() != 4 or q.shape[0] != pr.B or q.shape[1] % pr.heads or q.shape[3] != pr.d or 0 in q.shape:
+    _same_device(q, ("q", q), ("k", k), ("v", v), ("k_pool", k_pool), ("lengths", lengths),
+                 ("out", out), ("idx", idx), ("lse", lse), ("status", status))
+    if q.dim() != 4 or q.shape[0] != pr.B or q.shape[1] % pr.heads or q.shape[3] != pr.d or q.numel() == 0:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected ({pr.B}, a multiple of {pr.heads}, M, {pr.d})")
-    _expect(q, "q", tuple(q.shape), _FLOAT)
+    if q.dtype not in _FLOAT:
+        raise ValueError(f"q: dtype {q.dtype}, expected one of {_FLOAT}")
     for name, t in (("k", k), ("v", v)):
-        _expect(t, name, pr.permuted, q.dtype)
-    _expect(k_pool, "k_pool", pr.pooled, torch.float32)
+        if t.shape != pr.permuted or t.dtype != q.dtype:
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {pr.permuted} {q.dtype}")
+    if k_pool.shape != pr.pooled or k_pool.dtype != torch.float32:
+        raise ValueError(f"k_pool: {tuple(k_pool.shape)} {k_pool.dtype}, expected {pr.pooled} torch.float32")
     _expect(lengths, "lengths", (pr.B,), torch.int32)
     rows = tuple(q.shape[:3])
-    _expect(out, "out", tuple(q.shape), q.dtype)
+    _expect(out, "out", q.shape, q.dtype)
     _expect(idx, "idx", rows + (int(k_keep),), torch.int32)
     _expect(lse, "lse", rows, torch.float32)
     _expect_status(status)
@@ -795,11 +829,9 @@ def block_sparse_query_attn(q, k, v, k_pool, pr: Problem, k_keep: int, lengths=N
     out = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=dev)
     idx = idx if idx is not None else torch.empty(rows + (int(k_keep),), dtype=torch.int32, device=dev)
     lse = lse if lse is not None else torch.empty(rows, dtype=torch.float32, device=dev)
-    with _on(q):
-        _check(load().pa_query_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _dtype_code(q),
-                                    pr.shape, q.shape[1] // pr.heads, q.shape[2], int(k_keep),
-                                    _ptr(lengths), _ptr(out), _ptr(idx), _ptr(lse), _ptr(status),
-                                    _stream()))
+    _launch(q, load().pa_query_attn, q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pool.data_ptr(),
+            _dtype_code(q), pr.shape, q.shape[1] // pr.heads, q.shape[2], int(k_keep),
+            _addr(lengths), out.data_ptr(), idx.data_ptr(), lse.data_ptr(), _addr(status))
     return out, idx, lse
 
 
