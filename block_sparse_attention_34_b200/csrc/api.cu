@@ -16,8 +16,7 @@ cudaError_t launch_attn_sm100(const void* q, const void* k, const void* v, pa_dt
                               int k_max, const float* qs, const float* ks, const float* vs,
                               float p_levels, void* out, int32_t* status, bool permuted,
                               cudaStream_t s, const void* k_pool = nullptr,
-                              const void* v_pool = nullptr, pa_dtype pool_dtype = PA_F32,
-                              float* lse = nullptr);
+                              const void* v_pool = nullptr, pa_dtype pool_dtype = PA_F32);
 bool attn_sm100_supports(pa_dtype dt, const Grid& g);
 }  // namespace paro
 
@@ -616,13 +615,23 @@ pa_status pa_rope_reorder(const void* x, const int64_t* x_stride, void* x_perm, 
 
 // -------------------------------------------------------------- training --
 
+static pa_status train_limits(const paro::Grid& g) {
+  if (g.NB > 65535 || (int64_t)g.B * g.heads > 65535 ||
+      (int64_t)g.B * g.heads * g.Np >= ((int64_t)1 << 31))
+    return fail(PA_ERR_UNSUPPORTED,
+                "NB=%d or B*heads=%lld exceeds 65535, or B*heads*N_p reaches 2^31 rows", g.NB,
+                (long long)g.B * g.heads);
+  return PA_OK;
+}
+
 pa_status pa_block_sparse_attn_lse(const void* q, const void* k, const void* v, pa_dtype dtype,
-                                   uint32_t flags, pa_shape shape, const int8_t* perms,
-                                   const int32_t* idx, const int32_t* counts, int32_t k_max,
-                                   void* out, float* lse, int32_t* dev_status, void* stream) {
+                                   pa_shape shape, const int8_t* perms, const int32_t* idx,
+                                   const int32_t* counts, int32_t k_max, void* out, float* lse,
+                                   int32_t* dev_status, void* stream) {
   paro::Grid g;
   pa_status st = make_grid(shape, perms, true, &g);
   if (st != PA_OK) return st;
+  if ((st = train_limits(g)) != PA_OK) return st;
   if (dtype != PA_BF16)
     return fail(PA_ERR_UNSUPPORTED, "dtype %d: training attention takes PA_BF16", (int)dtype);
   PA_REQUIRE(q && k && v && out && lse, "q, k, v, out and lse must be non-NULL");
@@ -630,20 +639,23 @@ pa_status pa_block_sparse_attn_lse(const void* q, const void* k, const void* v, 
   PA_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(out),
              "q, k, v and out must be 16-byte aligned");
   PA_REQUIRE(k_max >= 0 && k_max <= g.NB, "k_max=%d must be in [0, NB=%d]", k_max, g.NB);
-  PA_REQUIRE((flags & ~PA_ATTN_PERMUTED) == 0, "unknown flags 0x%x", flags);
-  const bool permuted = (flags & PA_ATTN_PERMUTED) != 0;
   cudaStream_t s = (cudaStream_t)stream;
   const int64_t rows = (int64_t)g.B * g.heads * g.N;
   cudaError_t e;
   if (k_max == 0) {
     e = cudaMemsetAsync(out, 0, (size_t)rows * g.d * 2, s);
     if (e == cudaSuccess) e = paro::launch_fill(lse, -INFINITY, rows, s);
-  } else if (paro::attn_sm100_supports(dtype, g)) {
-    e = paro::launch_attn_sm100(q, k, v, dtype, g, idx, counts, k_max, nullptr, nullptr, nullptr,
-                                127.f, out, dev_status, permuted, s, nullptr, nullptr, PA_F32, lse);
   } else {
-    e = paro::launch_attn_mma(q, k, v, dtype, g, idx, counts, k_max, out, dev_status, permuted, s,
-                              nullptr, nullptr, lse);
+    paro::BwdArgs a = {};
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.idx = idx;
+    a.counts = counts;
+    a.k_max = k_max;
+    a.status = dev_status;
+    e = g.block == 128 ? paro::launch_fwd_lse_sm100(a, g, out, lse, s)
+                       : paro::launch_fwd_lse_mma(a, g, out, lse, s);
   }
   return cuda_status(e, "pa_block_sparse_attn_lse launch");
 }
@@ -666,17 +678,11 @@ BwdLayout bwd_layout(const paro::Grid& g) {
   l.bytes = l.mask + up((int64_t)g.B * g.heads * g.NB * l.words * 4);
   return l;
 }
-pa_status bwd_limits(const paro::Grid& g) {
-  if (g.NB > 65535 || (int64_t)g.B * g.heads > 65535)
-    return fail(PA_ERR_UNSUPPORTED, "NB=%d or B*heads=%lld exceeds 65535", g.NB,
-                (long long)g.B * g.heads);
-  return PA_OK;
-}
 }  // namespace
 
 int64_t pa_block_sparse_attn_backward_workspace(pa_shape shape) {
   paro::Grid g;
-  if (make_grid(shape, nullptr, false, &g) != PA_OK || bwd_limits(g) != PA_OK) return -1;
+  if (make_grid(shape, nullptr, false, &g) != PA_OK || train_limits(g) != PA_OK) return -1;
   return bwd_layout(g).bytes;
 }
 
@@ -690,7 +696,7 @@ pa_status pa_block_sparse_attn_backward(const void* dout, const void* q, const v
   paro::Grid g;
   pa_status st = make_grid(shape, perms, true, &g);
   if (st != PA_OK) return st;
-  if ((st = bwd_limits(g)) != PA_OK) return st;
+  if ((st = train_limits(g)) != PA_OK) return st;
   if (dtype != PA_BF16)
     return fail(PA_ERR_UNSUPPORTED, "dtype %d: training attention takes PA_BF16", (int)dtype);
   PA_REQUIRE(dout && q && k && v && out && lse && dq && dk && dv,
@@ -725,7 +731,7 @@ pa_status pa_block_sparse_attn_backward(const void* dout, const void* q, const v
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = paro::launch_bwd_prep(out, dout, lse, dlse, a, g, s);
   if (e == cudaSuccess)
-    e = paro::bwd_sm100_supports(g) ? paro::launch_bwd_sm100(a, g, s) : paro::launch_bwd_mma(a, g, s);
+    e = g.block == 128 ? paro::launch_bwd_sm100(a, g, s) : paro::launch_bwd_mma(a, g, s);
   return cuda_status(e, "pa_block_sparse_attn_backward launch");
 }
 

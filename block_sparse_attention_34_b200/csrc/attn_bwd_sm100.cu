@@ -470,10 +470,6 @@ cudaError_t launch_typed(const BwdArgs& a, const Grid& g, cudaStream_t s) {
 
 }  // namespace
 
-bool bwd_sm100_supports(const Grid& g) {
-  return g.block == kBlock && (int64_t)g.B * g.heads * g.Np < ((int64_t)1 << 31);
-}
-
 cudaError_t launch_bwd_sm100(const BwdArgs& a, const Grid& g, cudaStream_t s) {
   return g.d == 64 ? launch_typed<64>(a, g, s) : launch_typed<128>(a, g, s);
 }

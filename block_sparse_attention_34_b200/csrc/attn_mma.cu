@@ -202,8 +202,7 @@ __global__ void __launch_bounds__(BLOCK * 2)
                     const int32_t* __restrict__ idx, const int32_t* __restrict__ counts,
                     int k_max, float scale_log2, TIn* __restrict__ out,
                     int32_t* __restrict__ status, int permuted,
-                    const float* __restrict__ k_pool, const float* __restrict__ v_pool,
-                    float* __restrict__ lse) {
+                    const float* __restrict__ k_pool, const float* __restrict__ v_pool) {
   constexpr int LD = D + 8;  // padded row: conflict-free ldmatrix
   constexpr int NT = BLOCK / 8;  // n-tiles of S
   constexpr int DT = D / 8;  // n-tiles of O
@@ -320,14 +319,6 @@ __global__ void __launch_bounds__(BLOCK * 2)
   }
   const float i0 = l0 > 0.f ? 1.f / l0 : 0.f;
   const float i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-  if (lse != nullptr && lane % 4 == 0) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int p = i * BLOCK + warp * 16 + lane / 4 + 8 * u;
-      if (p < g.N)
-        lse[bh * g.N + natural_index(g, order, p)] = row_lse(u ? m1 : m0, u ? l1 : l0);
-    }
-  }
   __syncthreads();
   TIn* stage = reinterpret_cast<TIn*>(Ks);  // [BLOCK][D], fits in Ks+Vs
   const int r0 = warp * 16 + lane / 4;
@@ -357,7 +348,7 @@ template <typename TIn, int D, int BLOCK, bool kComp>
 cudaError_t launch_typed(const void* q, const void* k, const void* v, const Grid& g,
                          const int32_t* idx, const int32_t* counts, int k_max, void* out,
                          int32_t* status, bool permuted, const float* k_pool,
-                         const float* v_pool, float* lse, cudaStream_t s) {
+                         const float* v_pool, cudaStream_t s) {
   constexpr int LD = D + 8;
   const size_t smem = (size_t)3 * BLOCK * LD * sizeof(__nv_bfloat16) +
                       (kComp ? (size_t)kCompMaxNB / 8 : 0);
@@ -372,7 +363,7 @@ cudaError_t launch_typed(const void* q, const void* k, const void* v, const Grid
   kern<<<grid, BLOCK * 2, smem, s>>>(static_cast<const TIn*>(q), static_cast<const TIn*>(k),
                                      static_cast<const TIn*>(v), g, idx, counts, k_max,
                                      scale_log2, static_cast<TIn*>(out), status,
-                                     permuted ? 1 : 0, k_pool, v_pool, lse);
+                                     permuted ? 1 : 0, k_pool, v_pool);
   return cudaGetLastError();
 }
 
@@ -381,14 +372,14 @@ cudaError_t launch_typed(const void* q, const void* k, const void* v, const Grid
 cudaError_t launch_attn_mma(const void* q, const void* k, const void* v, pa_dtype dt,
                             const Grid& g, const int32_t* idx, const int32_t* counts, int k_max,
                             void* out, int32_t* status, bool permuted, cudaStream_t s,
-                            const float* k_pool, const float* v_pool, float* lse) {
+                            const float* k_pool, const float* v_pool) {
   const bool comp = k_pool != nullptr && v_pool != nullptr;
 #define PARO_A(T, D, BL)                                                                       \
   if (g.d == D && g.block == BL)                                                               \
     return comp ? launch_typed<T, D, BL, true>(q, k, v, g, idx, counts, k_max, out, status,    \
-                                               permuted, k_pool, v_pool, lse, s)               \
+                                               permuted, k_pool, v_pool, s)                    \
                 : launch_typed<T, D, BL, false>(q, k, v, g, idx, counts, k_max, out, status,   \
-                                                permuted, nullptr, nullptr, lse, s);
+                                                permuted, nullptr, nullptr, s);
   if (dt == PA_BF16) {
     PARO_A(__nv_bfloat16, 64, 64)
     PARO_A(__nv_bfloat16, 64, 128)

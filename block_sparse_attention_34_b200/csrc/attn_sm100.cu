@@ -1,5 +1,6 @@
 // Block-sparse flash attention on the 5th-generation tensor cores of sm_100a
-// (tcgen05.mma, accumulators in tensor memory), d = 128, block = 128, bf16.
+// (tcgen05.mma, accumulators in tensor memory), d = 128, block = 128, bf16
+// (and d = 64 for the forward pass of training).
 //
 // What it computes (SPADE, arXiv 2608.03335, Pith verdict page,
 // key_machinery (iii): a flash block-sparse attention kernel with an online
@@ -68,6 +69,7 @@
 // before the CTA exits.
 #include <type_traits>
 
+#include "bwd.cuh"
 #include "sm100.cuh"
 
 namespace paro {
@@ -219,7 +221,9 @@ __device__ __forceinline__ void copy_tile(uint32_t tile, const __nv_bfloat16* __
 // over the [B*heads*NB, d] rows; rows past a head's NB belong to the next
 // head and are masked like the blocks past NB, rows past the array's end
 // read as zero).
-template <bool kTma, bool kComp>
+// D: 128, or 64 (permuted inputs, no compensation: the forward pass of
+// training).  lse, if not NULL, receives each row's log-sum-exp.
+template <bool kTma, bool kComp, int D = kD>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_sm100_kernel(const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_k,
@@ -233,6 +237,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                       int32_t* __restrict__ status, const StallTest st,
                       const void* __restrict__ k_pool, const void* __restrict__ v_pool,
                       int pool_bf16, float* __restrict__ lse) {
+  constexpr int kD = D;
+  constexpr uint32_t kTile = kBlock * D * 2;
+  constexpr uint32_t kOffK = kOffQ + kTile, kOffV = kOffK + kStages * kTile;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // the operand tiles need 1024-byte alignment (the swizzle pattern repeats
   // every 8 rows of 128 bytes); dynamic shared memory starts at the window
@@ -339,8 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kTma) {
             if (lane == 0) {
               mbar_arrive_tx(bar(BQ), kTile);
-              tma_load_2d(base + kOffQ, &map_q, 0, row0 + i * kBlock, bar(BQ));
-              tma_load_2d(base + kOffQ + kHalf, &map_q, 64, row0 + i * kBlock, bar(BQ));
+#pragma unroll
+              for (int x = 0; x < kD / 64; ++x)
+                tma_load_2d(base + kOffQ + x * kHalf, &map_q, 64 * x, row0 + i * kBlock, bar(BQ));
             }
           } else {
             copy_tile(base + kOffQ, qh, g, order, i * kBlock, lane);
@@ -402,8 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kTma) {
             if (lane == 0) {
               mbar_arrive_tx(full, kTile);
-              tma_load_2d(ring + s * kTile, map, 0, row0 + kb * kBlock, full);
-              tma_load_2d(ring + s * kTile + kHalf, map, 64, row0 + kb * kBlock, full);
+#pragma unroll
+              for (int x = 0; x < kD / 64; ++x)
+                tma_load_2d(ring + s * kTile + x * kHalf, map, 64 * x, row0 + kb * kBlock, full);
             }
           } else {
             copy_tile(ring + s * kTile, src, g, order, kb * kBlock, lane);
@@ -640,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float alpha = need ? ex2(m_prev - m_j) : 1.f;
 #pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
+        for (int c0 = 0; c0 < kD; c0 += 32) {
           uint32_t orr[32];
           tmem_ld32(lane_addr + kColO + c0, orr);
 #pragma unroll
@@ -659,16 +668,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok && jg < n_tiles; jg += 2) ok = step(jg, std::true_type{});
     // ---- epilogue: add the groups' row sums (each relative to its own
     // latest reference; O is relative to the last tile's, the larger), then
-    // group g writes output columns 64g .. 64g+63 of the row at the natural
-    // position of its token
+    // group g writes output columns g d/2 .. + d/2 - 1 of the row at the
+    // natural position of its token
     const int p = i * kBlock + r;
     const int64_t nat = p < g.N ? bh * (int64_t)g.N + natural_index(g, order, p) : -1;
     __nv_bfloat16* orow = nat >= 0 ? out + nat * kD : nullptr;
     if (run && n_tiles == 0) {
       if (lse != nullptr && nat >= 0 && grp == 0) lse[nat] = -INFINITY;
       if (orow != nullptr)
-        for (int c = 0; c < 8; ++c)
-          reinterpret_cast<uint4*>(orow + grp * 64)[c] = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < kD / 16; ++c)
+          reinterpret_cast<uint4*>(orow + grp * (kD / 2))[c] = make_uint4(0, 0, 0, 0);
     } else if (ok && n_tiles > 0) {
       lsum[grp * 128 + r] = l;
       mref[grp * 128 + r] = m_mine;  // -inf for a group that saw no tile
@@ -688,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (okm) {
         tc_fence_after();
 #pragma unroll 1
-        for (int c0 = 0; c0 < 64; c0 += 32) {
-          const int col = grp * 64 + c0;
+        for (int c0 = 0; c0 < kD / 2; c0 += 32) {
+          const int col = grp * (kD / 2) + c0;
           uint32_t oa[32];
           tmem_ld32(lane_addr + kColO + col, oa);
           if (orow != nullptr) {
@@ -723,8 +732,7 @@ cudaError_t launch_typed(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
                          const CUtensorMap& mkp, const CUtensorMap& mvp, const void* q,
                          const void* k, const void* v, const Grid& g, const int32_t* idx,
                          const int32_t* counts, int k_max, void* out, int32_t* status,
-                         cudaStream_t s, const void* k_pool, const void* v_pool, int pool_bf16,
-                         float* lse) {
+                         cudaStream_t s, const void* k_pool, const void* v_pool, int pool_bf16) {
   if (kComp && g.NB > kCompMaxNB) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attn_sm100_kernel<kTma, kComp>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
@@ -734,11 +742,37 @@ cudaError_t launch_typed(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   attn_sm100_kernel<kTma, kComp><<<grid, kThreads, kSmemBytes, s>>>(
       mq, mk, mv, mkp, mvp, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
       static_cast<const __nv_bfloat16*>(v), g, idx, counts, k_max, scale_log2,
-      static_cast<__nv_bfloat16*>(out), status, stall_test(), k_pool, v_pool, pool_bf16, lse);
+      static_cast<__nv_bfloat16*>(out), status, stall_test(), k_pool, v_pool, pool_bf16,
+      nullptr);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_lse(const BwdArgs& a, const Grid& g, void* out, float* lse, cudaStream_t s) {
+  constexpr int kSmem = kOffQ + (1 + 2 * kStages) * kBlock * D * 2;
+  auto kern = attn_sm100_kernel<true, false, D>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const uint64_t rows = (uint64_t)g.B * g.heads * g.Np;
+  CUtensorMap mq{}, mk{}, mv{}, none{};
+  if (!encode_tile_map(&mq, a.q, rows, D, 2, 64, kBlock) ||
+      !encode_tile_map(&mk, a.k, rows, D, 2, 64, kBlock) ||
+      !encode_tile_map(&mv, a.v, rows, D, 2, 64, kBlock))
+    return cudaErrorInvalidValue;
+  kern<<<dim3(g.NB, g.B * g.heads), kThreads, kSmem, s>>>(
+      mq, mk, mv, none, none, a.q, a.k, a.v, g, a.idx, a.counts, a.k_max,
+      (float)(1.4426950408889634 / sqrt((double)D)), static_cast<__nv_bfloat16*>(out), a.status,
+      stall_test(), nullptr, nullptr, 0, lse);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t launch_fwd_lse_sm100(const BwdArgs& a, const Grid& g, void* out, float* lse,
+                                 cudaStream_t s) {
+  return g.d == 64 ? launch_lse<64>(a, g, out, lse, s) : launch_lse<128>(a, g, out, lse, s);
+}
 
 bool attn_sm100_supports(pa_dtype dt, const Grid& g) {
   return (dt == PA_BF16 || dt == PA_I8) && g.d == kD && g.block == kBlock &&
@@ -750,7 +784,7 @@ cudaError_t launch_attn_sm100(const void* q, const void* k, const void* v, pa_dt
                               int k_max, const float* qs, const float* ks, const float* vs,
                               float p_levels, void* out, int32_t* status, bool permuted,
                               cudaStream_t s, const void* k_pool, const void* v_pool,
-                              pa_dtype pool_dtype, float* lse) {
+                              pa_dtype pool_dtype) {
   if (!attn_sm100_supports(dt, g)) return cudaErrorInvalidValue;
   const bool comp = k_pool != nullptr && v_pool != nullptr;
   if (comp && dt != PA_BF16) return cudaErrorInvalidValue;
@@ -770,14 +804,14 @@ cudaError_t launch_attn_sm100(const void* q, const void* k, const void* v, pa_dt
         !encode_tile_map(&mv, v, rows, kD, 2, 64, kBlock))
       return cudaErrorInvalidValue;
     return comp ? launch_typed<true, true>(mq, mk, mv, mkp, mvp, q, k, v, g, idx, counts, k_max,
-                                           out, status, s, k_pool, v_pool, pool_bf16, lse)
+                                           out, status, s, k_pool, v_pool, pool_bf16)
                 : launch_typed<true, false>(mq, mk, mv, mkp, mvp, q, k, v, g, idx, counts, k_max,
-                                            out, status, s, nullptr, nullptr, 0, lse);
+                                            out, status, s, nullptr, nullptr, 0);
   }
   return comp ? launch_typed<false, true>(mq, mk, mv, mkp, mvp, q, k, v, g, idx, counts, k_max,
-                                          out, status, s, k_pool, v_pool, pool_bf16, lse)
+                                          out, status, s, k_pool, v_pool, pool_bf16)
               : launch_typed<false, false>(mq, mk, mv, mkp, mvp, q, k, v, g, idx, counts, k_max,
-                                           out, status, s, nullptr, nullptr, 0, lse);
+                                           out, status, s, nullptr, nullptr, 0);
 }
 
 }  // namespace paro

@@ -1,5 +1,5 @@
-// What the backward pass's kernel files share: the launch arguments and the
-// check of a kept list.
+// What the training kernels' files share: the launch arguments and the check
+// of a kept list.
 #pragma once
 
 #include "common.cuh"
@@ -34,10 +34,14 @@ __device__ __forceinline__ bool list_ok(const int32_t* __restrict__ ids, int cnt
 
 cudaError_t launch_bwd_prep(const void* out, const void* dout, const float* lse,
                             const float* dlse, const BwdArgs& a, const Grid& g, cudaStream_t s);
-// The tensor-core kernels of block 128 (attn_bwd_sm100.cu), the warp-level
-// ones of every shape (attn_bwd.cu).
-bool bwd_sm100_supports(const Grid& g);
+// The tcgen05 kernels of block 128 (attn_sm100.cu, attn_bwd_sm100.cu) and the
+// warp-level ones of block 64 (attn_train_mma.cu).  Of the arguments the
+// forward pass uses q, k, v, idx, counts, k_max and status.
+cudaError_t launch_fwd_lse_sm100(const BwdArgs& a, const Grid& g, void* out, float* lse,
+                                 cudaStream_t s);
 cudaError_t launch_bwd_sm100(const BwdArgs& a, const Grid& g, cudaStream_t s);
+cudaError_t launch_fwd_lse_mma(const BwdArgs& a, const Grid& g, void* out, float* lse,
+                               cudaStream_t s);
 cudaError_t launch_bwd_mma(const BwdArgs& a, const Grid& g, cudaStream_t s);
 
 }  // namespace paro

@@ -170,8 +170,7 @@ cudaError_t launch_quantize(const void* x, pa_dtype dt, const Grid& g, int8_t* x
 cudaError_t launch_attn_mma(const void* q, const void* k, const void* v, pa_dtype dt,
                             const Grid& g, const int32_t* idx, const int32_t* counts, int k_max,
                             void* out, int32_t* status, bool permuted, cudaStream_t s,
-                            const float* k_pool = nullptr, const float* v_pool = nullptr,
-                            float* lse = nullptr);
+                            const float* k_pool = nullptr, const float* v_pool = nullptr);
 cudaError_t launch_fill(float* x, float value, int64_t n, cudaStream_t s);
 // Rotary positions (rope.cu): make_rope_tab fills the table's layout and
 // returns its length in floats

@@ -99,8 +99,7 @@ def load():
         "pa_rope_apply": ([_P, _P, _P, _P, _I, PaShape, PaRope, _P, _P, _I, ctypes.c_uint32, _P,
                            _P], _I),
         "pa_rope_reorder": ([_P, _P, _P, _I, PaShape, _P, PaRope, _P, _P, _P], _I),
-        "pa_block_sparse_attn_lse": ([_P, _P, _P, _I, ctypes.c_uint32, PaShape, _P, _P, _P, _I, _P,
-                                      _P, _P, _P], _I),
+        "pa_block_sparse_attn_lse": ([_P, _P, _P, _I, PaShape, _P, _P, _P, _I, _P, _P, _P, _P], _I),
         "pa_block_sparse_attn_backward_workspace": ([PaShape], ctypes.c_int64),
         "pa_block_sparse_attn_backward": ([_P] * 7 + [_I, PaShape, _P, _P, _P, _I, _P, _P, _P, _P,
                                                       ctypes.c_int64, _P, _P], _I),
@@ -245,16 +244,16 @@ def reorder(x, pr: Problem, out=None, pool=None, with_pool=False):
     """Permuted copy [B, heads, N_p, d] of natural-order x; with
     ``with_pool`` (or a given ``pool`` buffer) also the block means, from
     the same read: returns (x_perm, pool)."""
-    _need_cuda(x, out, pool)
-    _expect(x, "x", pr.natural, _FLOAT)
+    _same_device(x, ("x", x), ("out", out), ("pool", pool))
+    if x.shape != pr.natural or x.dtype not in _FLOAT:
+        raise ValueError(f"x: {tuple(x.shape)} {x.dtype}, expected {pr.natural} and one of {_FLOAT}")
     _expect(out, "out", pr.permuted, x.dtype)
     _expect(pool, "pool", pr.pooled, torch.float32)
-    out = out if out is not None else torch.empty((pr.B, pr.heads, pr.N_p, pr.d), dtype=x.dtype,
-                                                  device=x.device)
+    out = out if out is not None else torch.empty(pr.permuted, dtype=x.dtype, device=x.device)
     if with_pool and pool is None:
-        pool = torch.empty((pr.B, pr.heads, pr.NB, pr.d), dtype=torch.float32, device=x.device)
-    _check(load().pa_reorder(_ptr(x), _ptr(out), _dtype_code(x), pr.shape, pr.perms_ptr,
-                             _ptr(pool), _stream()))
+        pool = torch.empty(pr.pooled, dtype=torch.float32, device=x.device)
+    _launch(x, load().pa_reorder, x.data_ptr(), out.data_ptr(), _dtype_code(x), pr.shape,
+            pr.perms_ptr, _addr(pool))
     return (out, pool) if (with_pool or pool is not None) else out
 
 
@@ -734,15 +733,14 @@ def _bf16(shape, *named):
             raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} torch.bfloat16")
 
 
-def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=None, status=None,
-                          permuted=True):
-    """:func:`block_sparse_attn` for bf16 q, k, v (by default the permuted
-    copies of :func:`reorder` or :func:`rope_reorder`), which also returns
-    the natural log-sum-exp of every row, [B, heads, N] float32 (-inf for a
-    row without kept blocks): the forward pass of training."""
+def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=None, status=None):
+    """:func:`block_sparse_attn` for bf16 permuted copies q, k, v
+    [B, heads, N_p, d] (:func:`reorder` or :func:`rope_reorder`), which also
+    returns the natural log-sum-exp of every row, [B, heads, N] float32 (-inf
+    for a row without kept blocks): the forward pass of training."""
     _same_device(q, ("q", q), ("k", k), ("v", v), ("idx", idx), ("counts", counts), ("out", out),
                  ("lse", lse), ("status", status))
-    _bf16(pr.permuted if permuted else pr.natural, ("q", q), ("k", k), ("v", v))
+    _bf16(pr.permuted, ("q", q), ("k", k), ("v", v))
     _check_lists(idx, counts, pr)
     _expect(out, "out", pr.natural, torch.bfloat16)
     _expect(lse, "lse", pr.natural[:3], torch.float32)
@@ -750,8 +748,7 @@ def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=
     out = out if out is not None else torch.empty(pr.natural, dtype=torch.bfloat16, device=q.device)
     lse = lse if lse is not None else torch.empty(pr.natural[:3], dtype=torch.float32, device=q.device)
     _launch(q, load().pa_block_sparse_attn_lse, q.data_ptr(), k.data_ptr(), v.data_ptr(), PA_BF16,
-            PA_ATTN_PERMUTED if permuted else 0, pr.shape, pr.perms_ptr, _addr(idx), _addr(counts),
-            idx.shape[3], out.data_ptr(), lse.data_ptr(), _addr(status))
+            pr.shape, pr.perms_ptr, _addr(idx), _addr(counts), idx.shape[3], out.data_ptr(), lse.data_ptr(), _addr(status))
     return out, lse
 
 

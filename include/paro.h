@@ -471,25 +471,28 @@ PA_API pa_status pa_rope_reorder(const void* x, const int64_t* x_stride, void* x
 
 /* ---- Training ---------------------------------------------------------
  *
- * pa_block_sparse_attn for dtype PA_BF16 (PA_ERR_UNSUPPORTED otherwise),
- * which also stores lse[b,h,n] = log sum_c exp(q_n . k_c / sqrt(d)) over
- * the row's kept keys (natural log; [B,heads,N] float, natural order; -inf
- * for a row without kept blocks).  out is the same, bit for bit. */
+ * The forward pass: pa_block_sparse_attn for dtype PA_BF16
+ * (PA_ERR_UNSUPPORTED otherwise) on the permuted copies q, k, v
+ * [B,heads,N_p,d] (pa_reorder's or pa_rope_reorder's output, pad rows zero),
+ * which also stores lse[b,h,n] = log sum_c exp(q_n . k_c / sqrt(d)) over the
+ * row's kept keys (natural log; [B,heads,N] float, natural order; -inf for a
+ * row without kept blocks).  Block 128 runs on the tcgen05 kernel (d = 128:
+ * out equals pa_block_sparse_attn's bit for bit), block 64 on mma.sync.
+ * NB <= 65535, B * heads <= 65535, B * heads * N_p < 2^31. */
 PA_API pa_status pa_block_sparse_attn_lse(const void* q, const void* k, const void* v,
-                                          pa_dtype dtype, uint32_t flags, pa_shape shape,
-                                          const int8_t* perms, const int32_t* idx,
-                                          const int32_t* counts, int32_t k_max, void* out,
-                                          float* lse, int32_t* dev_status, void* stream);
+                                          pa_dtype dtype, pa_shape shape, const int8_t* perms,
+                                          const int32_t* idx, const int32_t* counts,
+                                          int32_t k_max, void* out, float* lse,
+                                          int32_t* dev_status, void* stream);
 
 /* Bytes of workspace of pa_block_sparse_attn_backward, or -1 for a shape it
  * does not take. */
 PA_API int64_t pa_block_sparse_attn_backward_workspace(pa_shape shape);
 
-/* Gradients of pa_block_sparse_attn_lse (PA_BF16): with P = exp(S - lse) on
+/* The backward pass, gradients of pa_block_sparse_attn_lse (PA_BF16): with P = exp(S - lse) on
  * the kept tiles, D_n = dout_n . out_n - dlse_n, dS = P o (dout V^T - D),
  *   dq = dS K / sqrt(d),  dk = dS^T Q / sqrt(d),  dv = P^T dout.
- * q, k, v: the permuted copies [B,heads,N_p,d] that the forward pass took
- * with PA_ATTN_PERMUTED (pa_reorder's output, pad rows zero); dout, out, dq,
+ * q, k, v: the permuted copies that the forward pass took; dout, out, dq,
  * dk, dv [B,heads,N,d] bf16 natural order; lse, dlse (may be NULL: zero)
  * [B,heads,N] float.  idx, counts, k_max as in the forward pass; the
  * selection itself is not differentiated.  P and dS are rounded to bf16 for
@@ -498,8 +501,8 @@ PA_API int64_t pa_block_sparse_attn_backward_workspace(pa_shape shape);
  * malformed list is reported on dev_status (PA_ERR_DEVICE_CHECK): its rows
  * of dq are left unwritten and it adds nothing to dk and dv.
  * workspace: pa_block_sparse_attn_backward_workspace bytes, device memory,
- * 256-byte aligned, used by this call alone until it completes.
- * NB <= 65535, B * heads <= 65535. */
+ * 256-byte aligned, used by this call alone until it completes.  Limits as
+ * in the forward pass. */
 PA_API pa_status pa_block_sparse_attn_backward(
     const void* dout, const void* q, const void* k, const void* v, const void* out,
     const float* lse, const float* dlse, pa_dtype dtype, pa_shape shape, const int8_t* perms,
