@@ -89,16 +89,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 template <bool kKeys, int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    bwd_sm100_kernel(const __grid_constant__ CUtensorMap map_a1,
-                     const __grid_constant__ CUtensorMap map_a2,
-                     const __grid_constant__ CUtensorMap map_b1,
-                     const __grid_constant__ CUtensorMap map_b2, const float* __restrict__ nlse,
-                     const float* __restrict__ ndel, const __grid_constant__ Grid g,
-                     const int32_t* __restrict__ idx, const int32_t* __restrict__ counts,
-                     int k_max, const uint32_t* __restrict__ mask, int words, float scale,
-                     float scale_log2, __nv_bfloat16* __restrict__ g1,
-                     __nv_bfloat16* __restrict__ g2, int32_t* __restrict__ status) {
+__device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUtensorMap& map_a2,
+                                          const CUtensorMap& map_b1, const CUtensorMap& map_b2,
+                                          const BwdArgs& args, const Grid& g, float scale,
+                                          float scale_log2) {
+  const float* __restrict__ nlse = args.nlse;
+  const float* __restrict__ ndel = args.ndel;
+  const int words = args.words, k_max = args.k_max;
+  const int32_t *idx = args.idx, *counts = args.counts;
+  const uint32_t* __restrict__ mask = args.mask;
+  __nv_bfloat16* __restrict__ g1 = kKeys ? args.dk : args.dq;
+  __nv_bfloat16* __restrict__ g2 = args.dv;  // kKeys only
+  int32_t* status = args.status;
   constexpr uint32_t kTile = kBlock * D * 2;
   constexpr int kS1 = kB1Stages<kKeys>;
   constexpr uint32_t kOffA1 = kSmall, kOffA2 = kOffA1 + kTile, kOffB1 = kOffA2 + kTile,
@@ -439,17 +441,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// z = 0: the key blocks' CTAs, z = 1 the query blocks', which fill the SMs as
+// the first run out.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_sm100_kernel(const __grid_constant__ CUtensorMap map_q,
+                     const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ CUtensorMap map_do,
+                     const __grid_constant__ BwdArgs args, const __grid_constant__ Grid g,
+                     float scale, float scale_log2) {
+  if (blockIdx.z == 0)
+    bwd_block<true, D>(map_k, map_v, map_q, map_do, args, g, scale, scale_log2);
+  else
+    bwd_block<false, D>(map_q, map_do, map_k, map_v, args, g, scale, scale_log2);
+}
+
 template <int D>
 cudaError_t launch_typed(const BwdArgs& a, const Grid& g, cudaStream_t s) {
   constexpr uint32_t kTile = kBlock * D * 2;
-  constexpr int kSmemKeys = kSmall + (2 + kB1Stages<true> + kB2Stages) * kTile;
-  constexpr int kSmemQ = kSmall + (2 + kB1Stages<false> + kB2Stages) * kTile;
-  static_assert(kSmemQ <= kSmemOptIn, "shared memory");
-  auto kv = bwd_sm100_kernel<true, D>;
-  auto kq = bwd_sm100_kernel<false, D>;
-  cudaError_t e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemQ);
+  constexpr int kSmem = kSmall + (2 + kB1Stages<false> + kB2Stages) * kTile;
+  static_assert(kSmem <= kSmemOptIn && kB1Stages<true> <= kB1Stages<false>, "shared memory");
+  const cudaError_t e = opt_in_smem<bwd_sm100_kernel<D>>(kSmem);
   if (e != cudaSuccess) return e;
   const uint64_t rows = (uint64_t)g.B * g.heads * g.Np;
   CUtensorMap mq{}, mk{}, mv{}, md{};
@@ -458,13 +471,9 @@ cudaError_t launch_typed(const BwdArgs& a, const Grid& g, cudaStream_t s) {
       !encode_tile_map(&mv, a.v, rows, D, 2, 64, kBlock) ||
       !encode_tile_map(&md, a.dop, rows, D, 2, 64, kBlock))
     return cudaErrorInvalidValue;
-  const float scale = (float)(1.0 / sqrt((double)D));
-  const float scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
-  const dim3 grid(g.NB, g.B * g.heads);
-  kv<<<grid, kThreads, kSmemKeys, s>>>(mk, mv, mq, md, a.nlse, a.ndel, g, nullptr, nullptr, 0,
-                                       a.mask, a.words, scale, scale_log2, a.dk, a.dv, a.status);
-  kq<<<grid, kThreads, kSmemQ, s>>>(mq, md, mk, mv, a.nlse, a.ndel, g, a.idx, a.counts, a.k_max,
-                                    nullptr, 0, scale, scale_log2, a.dq, nullptr, a.status);
+  bwd_sm100_kernel<D><<<dim3(g.NB, g.B * g.heads, 2), kThreads, kSmem, s>>>(
+      mq, mk, mv, md, a, g, (float)(1.0 / sqrt((double)D)),
+      (float)(1.4426950408889634 / sqrt((double)D)));
   return cudaGetLastError();
 }
 

@@ -751,8 +751,7 @@ template <int D>
 cudaError_t launch_lse(const BwdArgs& a, const Grid& g, void* out, float* lse, cudaStream_t s) {
   constexpr int kSmem = kOffQ + (1 + 2 * kStages) * kBlock * D * 2;
   auto kern = attn_sm100_kernel<true, false, D>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t e = opt_in_smem<attn_sm100_kernel<true, false, D>>(kSmem);
   if (e != cudaSuccess) return e;
   const uint64_t rows = (uint64_t)g.B * g.heads * g.Np;
   CUtensorMap mq{}, mk{}, mv{}, none{};

@@ -4,8 +4,7 @@
 // of attn_bwd.cu.  (tcgen05 works on 128 rows at a time.)
 //
 // A CTA owns a block of 64 rows and goes over the 64-column tiles of its
-// list, the next tile on its way (cp.async, two stages) while it works on
-// this one.  Eight warps: warp w owns rows 16 (w % 4) .. +15 and the columns
+// list, the next tiles on their way (cp.async) while it works on this one.  Eight warps: warp w owns rows 16 (w % 4) .. +15 and the columns
 // 32 (w / 4) .. +31 of every tile; the two column halves keep their own sums
 // and join once at the end.  Such tiles are small (64 KFLOP a warp and
 // product at d = 64), so latency bounds a list's walk: with one tile in
@@ -19,6 +18,10 @@ namespace {
 
 constexpr int kBlock = 64;
 constexpr int kThreads = 256;
+// tiles of a list on their way or in use: their loads take longer than a
+// tile's work
+template <int D>
+constexpr int kStages = D == 64 ? 4 : 3;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void ldsm4(const void* p, uint32_t (&r)[4]) {
@@ -59,6 +62,10 @@ __device__ __forceinline__ void fetch_end() {
 template <int N>
 __device__ __forceinline__ void fetch_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int D>
+__device__ __forceinline__ int next_stage(int s) {
+  return s == kStages<D> - 1 ? 0 : s + 1;
 }
 
 // The A fragments of a warp's 16 rows (row0 on) at k-step ks of a tile.
@@ -127,7 +134,7 @@ __device__ __forceinline__ void join(float (&acc)[D / 8][4], float* pass, int ha
 
 // ---------------------------------------------------------------- forward --
 template <int D>
-constexpr int kFwdSmem = (1 + 4) * kTileElems<D> * 2;
+constexpr int kFwdSmem = (1 + 2 * kStages<D>) * kTileElems<D> * 2;
 static_assert(kFwdSmem<64> - kTileElems<64> * 2 >= 128 * (64 / 2) * 4, "join");
 static_assert(kFwdSmem<128> - kTileElems<128> * 2 >= 128 * (128 / 2) * 4, "join");
 
@@ -140,7 +147,7 @@ __global__ void __launch_bounds__(kThreads)
                    int32_t* __restrict__ status) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __nv_bfloat16* Qs = reinterpret_cast<__nv_bfloat16*>(smem_raw);
-  __nv_bfloat16* KV = Qs + kTileElems<D>;  // two stages of K, V
+  __nv_bfloat16* KV = Qs + kTileElems<D>;  // the stages of K, V
   __shared__ float maxima[2][kBlock], sums[2][kBlock];  // of the column halves
   const int t = blockIdx.x;
   const int64_t bh = blockIdx.y;
@@ -157,24 +164,28 @@ __global__ void __launch_bounds__(kThreads)
     fetch_wait<0>();
     return;
   }
-  auto fetch = [&](int e) {
+  auto fetch = [&](int e, int stage) {
     if (e < cnt) {
       const int64_t at = (head + (int64_t)__ldg(ids + e) * kBlock) * D;
-      __nv_bfloat16* to = KV + (e & 1) * 2 * kTileElems<D>;
+      __nv_bfloat16* to = KV + stage * 2 * kTileElems<D>;
       fetch_tile<D>(to, k + at);
       fetch_tile<D>(to + kTileElems<D>, v + at);
     }
     fetch_end();
   };
-  fetch(0);  // with Q
+#pragma unroll
+  for (int e = 0; e < kStages<D> - 1; ++e) fetch(e, e);  // the first with Q
   float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  int stage = 0;
   for (int e = 0; e < cnt; ++e) {
-    fetch(e + 1);
-    fetch_wait<1>();
+    fetch_wait<kStages<D> - 2>();
+    // this tile is here for every warp, and the one before it is consumed
     __syncthreads();
-    const __nv_bfloat16* Ks = KV + (e & 1) * 2 * kTileElems<D>;
+    fetch(e + kStages<D> - 1, stage == 0 ? kStages<D> - 1 : stage - 1);
+    const __nv_bfloat16* Ks = KV + stage * 2 * kTileElems<D>;
+    stage = next_stage<D>(stage);
     const __nv_bfloat16* Vs = Ks + kTileElems<D>;
     float s[4][4];
 #pragma unroll
@@ -241,7 +252,6 @@ __global__ void __launch_bounds__(kThreads)
         mma16816(o[n + 1], a, b[2], b[3]);
       }
     }
-    __syncthreads();  // the tile is consumed
   }
   fetch_wait<0>();
   // ---- join the column halves, normalise, store
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // --------------------------------------------------------------- backward --
 template <int D>
-constexpr int kBwdSmem = (2 + 4) * kTileElems<D> * 2 + 2 * 2 * kBlock * 4;
+constexpr int kBwdSmem = (2 + 2 * kStages<D>) * kTileElems<D> * 2 + kStages<D> * 2 * kBlock * 4;
 
 // kKeys: one CTA per key block, dK and dV (rows are keys: A1 = K, A2 = V;
 // streamed query blocks: B1 = Q, B2 = dO).  Otherwise one CTA per query
@@ -289,20 +299,21 @@ constexpr int kBwdSmem = (2 + 4) * kTileElems<D> * 2 + 2 * 2 * kBlock * 4;
 // the tile, G1 += dS B1 and (kKeys) G2 += P B2.  P and dS are rounded to bf16
 // for their products.
 template <int D, bool kKeys>
-__global__ void __launch_bounds__(kThreads)
-    bwd_mma_kernel(const __nv_bfloat16* __restrict__ a1, const __nv_bfloat16* __restrict__ a2,
-                   const __nv_bfloat16* __restrict__ b1, const __nv_bfloat16* __restrict__ b2,
-                   const float* __restrict__ nlse, const float* __restrict__ ndel,
-                   const __grid_constant__ Grid g, const int32_t* __restrict__ idx,
-                   const int32_t* __restrict__ counts, int k_max,
-                   const uint32_t* __restrict__ mask, int words, float scale,
-                   __nv_bfloat16* __restrict__ g1, __nv_bfloat16* __restrict__ g2,
-                   int32_t* __restrict__ status) {
+__device__ __forceinline__ void bwd_block(const BwdArgs& args, const Grid& g, float scale) {
+  const __nv_bfloat16* __restrict__ a1 = kKeys ? args.k : args.q;
+  const __nv_bfloat16* __restrict__ a2 = kKeys ? args.v : args.dop;
+  const __nv_bfloat16* __restrict__ b1 = kKeys ? args.q : args.k;
+  const __nv_bfloat16* __restrict__ b2 = kKeys ? args.dop : args.v;
+  const float *nlse = args.nlse, *ndel = args.ndel;
+  const int words = args.words, k_max = args.k_max;
+  const int32_t *idx = args.idx, *counts = args.counts;
+  const uint32_t* mask = args.mask;
+  int32_t* status = args.status;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __nv_bfloat16* A1 = reinterpret_cast<__nv_bfloat16*>(smem_raw);
   __nv_bfloat16* A2 = A1 + kTileElems<D>;
-  __nv_bfloat16* Bs = A2 + kTileElems<D>;  // two stages of B1, B2
-  float* stats = reinterpret_cast<float*>(Bs + 4 * kTileElems<D>);  // kKeys: [stage][-lse, -D][64]
+  __nv_bfloat16* Bs = A2 + kTileElems<D>;  // the stages of B1, B2
+  float* stats = reinterpret_cast<float*>(Bs + 2 * kStages<D> * kTileElems<D>);  // kKeys: [stage][-lse, -D][64]
   const int t = blockIdx.x;  // this CTA's block of rows
   const int64_t bh = blockIdx.y;
   const int order = g.perm[(int)(bh % g.heads)];
@@ -371,13 +382,20 @@ __global__ void __launch_bounds__(kThreads)
       acc1[n][e] = 0.f;
       if constexpr (kKeys) acc2[n][e] = 0.f;
     }
-  int j = next(), stage = 0;
-  fetch(j, 0);  // with A1, A2
-  while (j >= 0) {
-    const int ahead = next();
-    fetch(ahead, stage ^ 1);
-    fetch_wait<1>();
+  int tiles[kStages<D>];  // this tile and those on their way
+#pragma unroll
+  for (int u = 0; u < kStages<D> - 1; ++u) {
+    tiles[u] = next();
+    fetch(tiles[u], u);  // the first with A1, A2
+  }
+  int stage = 0;
+  while (tiles[0] >= 0) {
+    const int j = tiles[0];
+    fetch_wait<kStages<D> - 2>();
+    // this tile is here for every warp, and the one before it is consumed
     __syncthreads();
+    tiles[kStages<D> - 1] = next();
+    fetch(tiles[kStages<D> - 1], stage == 0 ? kStages<D> - 1 : stage - 1);
     const __nv_bfloat16* B1 = Bs + stage * 2 * kTileElems<D>;
     const __nv_bfloat16* B2 = B1 + kTileElems<D>;
     float x[4][4], y[4][4];
@@ -446,9 +464,9 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     }
-    __syncthreads();  // the tile is consumed
-    j = ahead;
-    stage ^= 1;
+#pragma unroll
+    for (int u = 0; u < kStages<D> - 1; ++u) tiles[u] = tiles[u + 1];
+    stage = next_stage<D>(stage);
   }
   fetch_wait<0>();
   auto finish = [&](float (&acc)[D / 8][4], float mul, __nv_bfloat16* dst) {
@@ -459,17 +477,26 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
   };
   __syncthreads();  // A1 may have come without a tile to wait for
-  finish(acc1, scale, g1);
-  if constexpr (kKeys) finish(acc2, 1.f, g2);
+  finish(acc1, scale, kKeys ? args.dk : args.dq);
+  if constexpr (kKeys) finish(acc2, 1.f, args.dv);
+}
+
+// z = 0: the key blocks' CTAs, z = 1 the query blocks'.
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    bwd_mma_kernel(const __grid_constant__ BwdArgs args, const __grid_constant__ Grid g,
+                   float scale) {
+  if (blockIdx.z == 0)
+    bwd_block<D, true>(args, g, scale);
+  else
+    bwd_block<D, false>(args, g, scale);
 }
 
 template <int D>
 cudaError_t launch_fwd(const BwdArgs& a, const Grid& g, void* out, float* lse, cudaStream_t s) {
-  auto kern = fwd_lse_kernel<D>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFwdSmem<D>);
+  const cudaError_t e = opt_in_smem<fwd_lse_kernel<D>>(kFwdSmem<D>);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(g.NB, g.B * g.heads), kThreads, kFwdSmem<D>, s>>>(
+  fwd_lse_kernel<D><<<dim3(g.NB, g.B * g.heads), kThreads, kFwdSmem<D>, s>>>(
       a.q, a.k, a.v, g, a.idx, a.counts, a.k_max, (float)(1.4426950408889634 / sqrt((double)D)),
       static_cast<__nv_bfloat16*>(out), lse, a.status);
   return cudaGetLastError();
@@ -477,18 +504,10 @@ cudaError_t launch_fwd(const BwdArgs& a, const Grid& g, void* out, float* lse, c
 
 template <int D>
 cudaError_t launch_bwd(const BwdArgs& a, const Grid& g, cudaStream_t s) {
-  const float scale = (float)(1.0 / sqrt((double)D));
-  const dim3 grid(g.NB, g.B * g.heads);
-  auto kv = bwd_mma_kernel<D, true>;
-  auto kq = bwd_mma_kernel<D, false>;
-  cudaError_t e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem<D>);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem<D>);
+  const cudaError_t e = opt_in_smem<bwd_mma_kernel<D>>(kBwdSmem<D>);
   if (e != cudaSuccess) return e;
-  kv<<<grid, kThreads, kBwdSmem<D>, s>>>(a.k, a.v, a.q, a.dop, a.nlse, a.ndel, g, nullptr, nullptr,
-                                         0, a.mask, a.words, scale, a.dk, a.dv, a.status);
-  kq<<<grid, kThreads, kBwdSmem<D>, s>>>(a.q, a.dop, a.k, a.v, a.nlse, a.ndel, g, a.idx, a.counts,
-                                         a.k_max, nullptr, 0, scale, a.dq, nullptr, a.status);
+  bwd_mma_kernel<D><<<dim3(g.NB, g.B * g.heads, 2), kThreads, kBwdSmem<D>, s>>>(
+      a, g, (float)(1.0 / sqrt((double)D)));
   return cudaGetLastError();
 }
 

@@ -4,7 +4,25 @@
 
 #include "common.cuh"
 
+#include <atomic>
+
 namespace paro {
+
+// Opts kernel Kern into `bytes` of dynamic shared memory on the current
+// device, once for each size that grows (the attribute outlives the call;
+// setting it every time is a microsecond of a small call).
+template <auto Kern>
+cudaError_t opt_in_smem(int bytes) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> done[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kDevices && done[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < kDevices) done[dev].store(bytes, std::memory_order_relaxed);
+  return e;
+}
 
 struct BwdArgs {
   const __nv_bfloat16 *q, *k, *v;  // permuted [B*heads, Np, d]

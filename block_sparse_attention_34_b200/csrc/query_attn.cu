@@ -27,6 +27,7 @@
 // fp32 arithmetic throughout.
 #include <type_traits>
 
+#include "bwd.cuh"
 #include "sm100.cuh"
 
 namespace paro {
@@ -838,7 +839,7 @@ cudaError_t launch_units(const void* q, const void* k, const void* v, const floa
                          const int32_t* lengths, void* out, int32_t* idx, float* lse,
                          int32_t* status, cudaStream_t s) {
   auto kern = query_attn_kernel<T, D, kUnits>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = opt_in_smem<query_attn_kernel<T, D, kUnits>>(smem);
   if (e == cudaSuccess && C > 8)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;

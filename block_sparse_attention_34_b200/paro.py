@@ -145,14 +145,15 @@ def _need_cuda(*ts):
     dev = None
     for t in ts:
         if t is not None:
-            if not t.is_cuda:
+            i = t.get_device()
+            if i < 0:
                 raise ValueError("tensors must be on a CUDA device (no CPU path)")
             if not t.is_contiguous():
                 raise ValueError("tensors must be contiguous")
             if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on different devices ({dev} and {t.device})")
+                dev = i
+            elif i != dev:
+                raise ValueError(f"tensors on different devices (cuda:{dev} and cuda:{i})")
 
 
 _FLOAT = (torch.float32, torch.bfloat16)
@@ -164,7 +165,7 @@ def _expect(t, name, shape, dtypes):
     shape implies, so a smaller buffer must never reach it."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(int(x) for x in shape):
+    if t.shape != shape and tuple(t.shape) != tuple(int(x) for x in shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if isinstance(dtypes, torch.dtype):
         dtypes = (dtypes,)
@@ -194,26 +195,14 @@ class Problem:
         self._perms = np.ascontiguousarray(p)
         self.shape = PaShape(self.B, self.heads, self.F, self.H, self.W, self.d, self.block)
         self.perms_ptr = self._perms.ctypes.data_as(ctypes.c_void_p)
-
-    @property
-    def natural(self):
-        return (self.B, self.heads, self.N, self.d)
-
-    @property
-    def permuted(self):
-        return (self.B, self.heads, self.N_p, self.d)
-
-    @property
-    def pooled(self):
-        return (self.B, self.heads, self.NB, self.d)
-
-    @property
-    def square(self):
-        return (self.B, self.heads, self.NB, self.NB)
-
-    @property
-    def per_block(self):
-        return (self.B, self.heads, self.NB)
+        self.workspace = None  # bytes of the backward pass's workspace, once asked for
+        # tensor shapes of the call
+        self.natural = (self.B, self.heads, self.N, self.d)
+        self.rows = (self.B, self.heads, self.N)
+        self.permuted = (self.B, self.heads, self.N_p, self.d)
+        self.pooled = (self.B, self.heads, self.NB, self.d)
+        self.square = (self.B, self.heads, self.NB, self.NB)
+        self.per_block = (self.B, self.heads, self.NB)
 
     @classmethod
     def from_qkv(cls, q, grid, perms, block):
@@ -244,7 +233,7 @@ def reorder(x, pr: Problem, out=None, pool=None, with_pool=False):
     """Permuted copy [B, heads, N_p, d] of natural-order x; with
     ``with_pool`` (or a given ``pool`` buffer) also the block means, from
     the same read: returns (x_perm, pool)."""
-    _same_device(x, ("x", x), ("out", out), ("pool", pool))
+    _need_cuda(x, out, pool)
     if x.shape != pr.natural or x.dtype not in _FLOAT:
         raise ValueError(f"x: {tuple(x.shape)} {x.dtype}, expected {pr.natural} and one of {_FLOAT}")
     _expect(out, "out", pr.permuted, x.dtype)
@@ -545,20 +534,20 @@ def round_bf16(x, out=None):
     return out
 
 
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _launch(t, fn, *args):
     """fn(*args, stream) on the device of ``t`` and its current stream."""
     i = t.get_device()
-    if i == torch.cuda.current_device():
+    if i == _current_device():
         status = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(i):
             status = fn(*args, _raw_stream(i))
     if status != PA_OK:
         raise ParoError(status, load().pa_last_error().decode())
-
-
-def _raw_stream(device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _same_device(t, *named):
@@ -570,7 +559,7 @@ def _same_device(t, *named):
     for name, u in named:
         if u is None:
             continue
-        if u.get_device() != i:
+        if u is not t and u.get_device() != i:
             raise ValueError(f"{name}: on {u.device}, expected {t.device}")
         if not u.is_contiguous():
             raise ValueError(f"{name}: tensors must be contiguous")
@@ -743,10 +732,10 @@ def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=
     _bf16(pr.permuted, ("q", q), ("k", k), ("v", v))
     _check_lists(idx, counts, pr)
     _expect(out, "out", pr.natural, torch.bfloat16)
-    _expect(lse, "lse", pr.natural[:3], torch.float32)
+    _expect(lse, "lse", pr.rows, torch.float32)
     _expect_status(status)
     out = out if out is not None else torch.empty(pr.natural, dtype=torch.bfloat16, device=q.device)
-    lse = lse if lse is not None else torch.empty(pr.natural[:3], dtype=torch.float32, device=q.device)
+    lse = lse if lse is not None else torch.empty(pr.rows, dtype=torch.float32, device=q.device)
     _launch(q, load().pa_block_sparse_attn_lse, q.data_ptr(), k.data_ptr(), v.data_ptr(), PA_BF16,
             pr.shape, pr.perms_ptr, _addr(idx), _addr(counts), idx.shape[3], out.data_ptr(), lse.data_ptr(), _addr(status))
     return out, lse
@@ -766,7 +755,7 @@ def block_sparse_attn_backward(dout, q, k, v, out, lse, pr: Problem, idx, counts
     _bf16(pr.permuted, ("q", q), ("k", k), ("v", v))
     _bf16(pr.natural, ("dout", dout), ("out", out), ("dq", dq), ("dk", dk), ("dv", dv))
     for name, t in (("lse", lse), ("dlse", dlse)):
-        _expect(t, name, pr.natural[:3], torch.float32)
+        _expect(t, name, pr.rows, torch.float32)
     _check_lists(idx, counts, pr)
     _expect_status(status)
     dq, dk, dv = (t if t is not None else torch.empty_like(out) for t in (dq, dk, dv))
@@ -783,10 +772,12 @@ def block_sparse_attn_backward(dout, q, k, v, out, lse, pr: Problem, idx, counts
 
 def backward_workspace(pr: Problem) -> int:
     """Bytes of workspace of :func:`block_sparse_attn_backward`."""
-    n = load().pa_block_sparse_attn_backward_workspace(pr.shape)
-    if n < 0:
-        raise ParoError(PA_ERR_UNSUPPORTED, load().pa_last_error().decode())
-    return n
+    if pr.workspace is None:
+        n = load().pa_block_sparse_attn_backward_workspace(pr.shape)
+        if n < 0:
+            raise ParoError(PA_ERR_UNSUPPORTED, load().pa_last_error().decode())
+        pr.workspace = n
+    return pr.workspace
 
 
 def block_sparse_query_attn(q, k, v, k_pool, pr: Problem, k_keep: int, lengths=None, out=None,
