@@ -1,0 +1,95 @@
+"""Differentiable forms of the library's operators, for training a video
+DiT: rotary positions and block-sparse attention as torch.autograd functions.
+
+Argument handling only, as in :mod:`paro`: every forward and backward step
+runs in the library's kernels on the current torch stream.  The choice of the
+kept blocks is not differentiated.  A step captured into a CUDA graph needs
+leaves that no eager autograd graph still holds, as everywhere in
+torch.autograd: it would wait for that graph's stream, which a capture
+forbids.
+"""
+
+from __future__ import annotations
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import paro
+
+
+def _rows(g):
+    """A gradient as the library takes it: rows contiguous and aligned."""
+    e = 16 // g.element_size()
+    fine = g.stride(3) == 1 and g.data_ptr() % 16 == 0 and all(g.stride(i) % e == 0 for i in range(3))
+    return g if fine else g.contiguous()
+
+
+class _Rope3d(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, rope, positions, inverse, status):
+        ctx.rope, ctx.inverse, ctx.status = rope, inverse, status
+        ctx.save_for_backward(positions)
+        return paro.rope3d(x, rope, positions=positions, inverse=inverse, status=status)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        (positions,) = ctx.saved_tensors
+        return paro.rope3d(_rows(g), ctx.rope, positions=positions, inverse=not ctx.inverse,
+                           status=ctx.status), None, None, None, None
+
+
+def rope3d(x, rope, positions=None, inverse=False, status=None):
+    """:func:`paro.rope3d`, differentiable in x."""
+    return _Rope3d.apply(x, rope, positions, inverse, status)
+
+
+class _SparseAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, pr, idx, counts, density, rope, status):
+        if rope is None:
+            q, k = q.contiguous(), k.contiguous()
+            qp, kp = (paro.reorder(x, pr, with_pool=idx is None) for x in (q, k))
+        else:
+            qp, kp = (paro.rope_reorder(_rows(x), rope, pr, with_pool=idx is None) for x in (q, k))
+        vp = paro.reorder(v.contiguous(), pr)
+        if idx is None:
+            (qp, q_pool), (kp, k_pool) = qp, kp
+            idx = paro.select_topk(paro.score_pooled(q_pool, k_pool, pr), pr,
+                                   paro.k_for_density(pr.NB, density))
+        out, lse = paro.block_sparse_attn_lse(qp, kp, vp, pr, idx, counts, status=status)
+        ctx.pr, ctx.rope, ctx.status = pr, rope, status
+        ctx.save_for_backward(qp, kp, vp, out, lse, idx, counts)
+        ctx.set_materialize_grads(False)
+        return out, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, dlse):
+        qp, kp, vp, out, lse, idx, counts = ctx.saved_tensors
+        if dout is None and dlse is None:
+            return (None,) * 9
+        dout = torch.zeros_like(out) if dout is None else dout.contiguous()
+        dlse = None if dlse is None else dlse.contiguous()
+        dq, dk, dv = paro.block_sparse_attn_backward(dout, qp, kp, vp, out, lse, ctx.pr, idx, counts,
+                                                     dlse=dlse, status=ctx.status)
+        if ctx.rope is not None:
+            grid = (ctx.pr.F, ctx.pr.H, ctx.pr.W)
+            for g in (dq, dk):
+                paro.rope3d(g, ctx.rope, grid=grid, inverse=True, out=g)
+        return dq, dk, dv, None, None, None, None, None, None
+
+
+def sparse_attention(q, k, v, pr, idx=None, counts=None, density=None, rope=None, status=None):
+    """Block-sparse attention of bf16 q, k, v [B, heads, N, d], natural token
+    order, differentiable in the three: returns (out, lse).
+
+    ``idx`` (and ``counts``): the kept blocks of every query block, or, with
+    ``density`` instead, the library's top-k of the pooled block scores.
+    ``rope`` (:class:`paro.RopeTable`): q and k are rotated on the way into
+    their heads' orders, and their gradients back."""
+    if (idx is None) == (density is None):
+        raise ValueError("give either idx or density")
+    if idx is None and counts is not None:
+        raise ValueError("counts go with idx")
+    return _SparseAttention.apply(q, k, v, pr, idx, counts, density, rope, status)

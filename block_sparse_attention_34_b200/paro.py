@@ -650,15 +650,15 @@ def _dense_rows(t):
     return True
 
 
-def rope3d(x, rope: RopeTable, positions=None, inverse=False, out=None, status=None):
+def rope3d(x, rope: RopeTable, positions=None, inverse=False, out=None, status=None, grid=None):
     """Rotary positions with three axes of x [B, heads, N, d].
 
     Rows must be contiguous and start at multiples of 16 bytes; batch, head
     and token strides are free, so the projection's [B, N, heads, d] goes in
-    as ``.transpose(1, 2)``.  Token n sits at its place in the table's grid
-    (N = frames * height * width of ``rope.extent``), or at ``positions``
-    (int32 [N, 3] or [B, N, 3], contiguous; a coordinate outside the table is
-    reported on ``status`` and its rows stay unwritten).  ``inverse`` turns
+    as ``.transpose(1, 2)``.  Token n sits at its place in ``grid`` (frames,
+    height, width; by default ``rope.extent``, which has to cover it), or at
+    ``positions`` (int32 [N, 3] or [B, N, 3], contiguous; a coordinate
+    outside the table is reported on ``status`` and its rows stay unwritten).  ``inverse`` turns
     back: the gradient's rotation.  ``out``: any non-overlapping strides, or
     x itself (not a tensor that shares only part of x's memory); contiguous
     by default."""
@@ -666,11 +666,13 @@ def rope3d(x, rope: RopeTable, positions=None, inverse=False, out=None, status=N
     _same_device(x, ("positions", positions), ("status", status))
     B, heads, N, d = x.shape
     if positions is None:
-        F, H, W = rope.extent
+        F, H, W = rope.extent if grid is None else grid
         if F * H * W != N:
-            raise ValueError(f"x has {N} tokens, the table's grid {rope.extent}: give positions")
+            raise ValueError(f"x has {N} tokens, the grid {(F, H, W)}: give grid or positions")
         batched = 0
     else:
+        if grid is not None:
+            raise ValueError("grid or positions, not both")
         F, H, W = 1, 1, N
         batched = int(positions.dim() == 3)
         if positions.shape != ((B, N, 3) if batched else (N, 3)) or positions.dtype != torch.int32:
@@ -836,7 +838,7 @@ def choose_orders_sics(q, k, grid, block):
 
 def attention(q, k, v, grid, perms, block, density, int8=False, baseline=False, status=None,
               permuted=True, int4_pv=False, selection="topk", top_p=0.0, window=-1,
-              compensate=False, p_tile=None):
+              compensate=False, p_tile=None, rope=None):
     """The whole path for one call: reorder with block means (one read of
     q, k, v) -> pooled block scores -> kept blocks -> block-sparse attention
     over the permuted tiles, stored back in natural order.
@@ -853,14 +855,25 @@ def attention(q, k, v, grid, perms, block, density, int8=False, baseline=False, 
     reorder pass (the kernel gathers token rows); ``baseline=True`` runs the
     mma.sync comparison kernel.  ``compensate`` adds PASA's grouped
     first-order compensation of the unselected blocks (bf16 / fp32 only;
-    :func:`block_sparse_attn_compensated`).  Returns (out, idx) — with the
-    hybrid filter, idx is (idx, counts)."""
+    :func:`block_sparse_attn_compensated`).  ``rope`` (:class:`RopeTable`):
+    q and k are rotated first, on the way into the heads' orders where the
+    path reorders them.  Returns (out, idx) — with the hybrid filter, idx is
+    (idx, counts)."""
+    if rope is not None and (isinstance(perms, str) or int8 or baseline or not (permuted or compensate)):
+        # the step that comes first reads q and k in their natural order
+        q, k = (rope3d(x, rope, grid=grid) for x in (q, k))
+        rope = None
     if isinstance(perms, str):
         if perms != "sics":
             raise ValueError(f"perms={perms!r}: order ids or 'sics'")
         perms = choose_orders_sics(q, k, grid, block)
     pr = Problem.from_qkv(q, grid, perms, block)
     kk = k_for_density(pr.NB, density)
+
+    def into_order(x):
+        if rope is None:
+            return reorder(x, pr, with_pool=True)
+        return rope_reorder(x, rope, pr, with_pool=True)
 
     def select(scores):
         if selection == "hybrid":
@@ -872,8 +885,8 @@ def attention(q, k, v, grid, perms, block, density, int8=False, baseline=False, 
     if compensate:
         if int8:
             raise ValueError("compensate runs on bf16 / fp32 inputs")
-        qp, q_pool = reorder(q, pr, with_pool=True)
-        kp, k_pool = reorder(k, pr, with_pool=True)
+        qp, q_pool = into_order(q)
+        kp, k_pool = into_order(k)
         vp, v_pool = reorder(v, pr, with_pool=True)
         idx, counts = select(score_pooled(q_pool, k_pool, pr))
         if q.dtype == torch.bfloat16 and pr.d == 128 and pr.block == 128:
@@ -889,8 +902,8 @@ def attention(q, k, v, grid, perms, block, density, int8=False, baseline=False, 
         out = block_sparse_attn(q8, k8, v8, pr, idx, counts, scales=(qs, ks, vs), status=status,
                                 p4=int4_pv, p_tile=int4_pv if p_tile is None else p_tile)
     elif permuted and not baseline:
-        qp, q_pool = reorder(q, pr, with_pool=True)
-        kp, k_pool = reorder(k, pr, with_pool=True)
+        qp, q_pool = into_order(q)
+        kp, k_pool = into_order(k)
         vp = reorder(v, pr)
         idx, counts = select(score_pooled(q_pool, k_pool, pr))
         out = block_sparse_attn(qp, kp, vp, pr, idx, counts, status=status, permuted=True)

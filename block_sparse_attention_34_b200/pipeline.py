@@ -5,6 +5,7 @@ Launch sequence of :meth:`Pipeline.run` (every step through the C ABI, on the
 current torch stream; the status word is cleared first, by a memset):
 
   bf16:  reorder+pool(q), reorder+pool(k), reorder(v)  -- one HBM pass each
+         (with rope: rotated in the same pass; the other paths rotate q, k first)
          score_pooled -> select_topk (or select_hybrid: diagonal, window,
          Top-K and Top-P with per-row counts) -> block_sparse_attn(permuted tiles)
   int8:  quantize+pool(q), quantize+pool(k), quantize(v)  (v to 4 bits with int4_pv)
@@ -25,7 +26,7 @@ from . import paro
 class Pipeline:
     def __init__(self, B, heads, grid, d, block, perms, density, dtype=torch.bfloat16,
                  device="cuda", int8=False, baseline=False, selection="topk", top_p=0.0,
-                 window=-1, int4_pv=False, p_tile=None):
+                 window=-1, int4_pv=False, p_tile=None, rope=None):
         self.pr = paro.Problem(B, heads, grid, d, block, perms)
         pr = self.pr
         self.k = paro.k_for_density(pr.NB, density)
@@ -38,7 +39,12 @@ class Pipeline:
         self.selection = selection
         self.top_p = float(top_p)
         self.window = int(window)
+        # rotary positions of q and k (paro.RopeTable): fused with the
+        # reorder, or into buffers of their own where there is none
+        self.rope = rope
         dev = torch.device(device)
+        if rope is not None and (self.int8 or baseline):
+            self.rotated = [torch.empty(pr.natural, dtype=dtype, device=dev) for _ in range(2)]
         if self.int8:
             self.xq = [torch.empty((B, heads, pr.N_p, d), dtype=torch.int8, device=dev) for _ in range(3)]
             self.sc = [torch.empty((B, heads, pr.NB), dtype=torch.float32, device=dev) for _ in range(3)]
@@ -60,10 +66,22 @@ class Pipeline:
     @property
     def launches(self) -> int:
         """Kernel launches of one :meth:`run` (all of them this library's)."""
-        return 5 if self.baseline else 6
+        n = 5 if self.baseline else 6
+        return n + 2 if self.rope is not None and (self.int8 or self.baseline) else n
+
+    def _rotate(self, q, k):
+        """q, k as the path's first step takes them: rotated here when that
+        step does not rotate."""
+        if self.rope is None or not (self.int8 or self.baseline):
+            return q, k
+        grid = (self.pr.F, self.pr.H, self.pr.W)
+        for x, y in zip((q, k), self.rotated):
+            paro.rope3d(x, self.rope, out=y, grid=grid)
+        return self.rotated
 
     def select(self, q, k, v):
         pr = self.pr
+        q, k = self._rotate(q, k)
         if self.int8:
             paro.quantize_int8(q, pr, x_q=self.xq[0], scales=self.sc[0], pool=self.q_pool)
             paro.quantize_int8(k, pr, x_q=self.xq[1], scales=self.sc[1], pool=self.k_pool)
@@ -73,8 +91,11 @@ class Pipeline:
         elif self.baseline:
             paro.block_score(q, k, pr, self.q_pool, self.k_pool, self.scores)
         else:
-            paro.reorder(q, pr, out=self.xp[0], pool=self.q_pool)
-            paro.reorder(k, pr, out=self.xp[1], pool=self.k_pool)
+            for x, xp, pool in zip((q, k), self.xp, (self.q_pool, self.k_pool)):
+                if self.rope is None:
+                    paro.reorder(x, pr, out=xp, pool=pool)
+                else:
+                    paro.rope_reorder(x, self.rope, pr, out=xp, pool=pool)
             paro.reorder(v, pr, out=self.xp[2])
             paro.score_pooled(self.q_pool, self.k_pool, pr, scores=self.scores)
         if self.selection == "hybrid":
@@ -90,6 +111,8 @@ class Pipeline:
                                    out=self.out, status=self.status, p4=self.int4_pv,
                                    p_tile=self.p_tile)
         elif self.baseline:
+            if self.rope is not None:  # as select() left them
+                q, k = self.rotated
             paro.block_sparse_attn(q, k, v, pr, self.idx, self.counts, out=self.out,
                                    status=self.status, baseline=True)
         else:
