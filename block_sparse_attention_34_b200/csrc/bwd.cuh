@@ -9,9 +9,10 @@
 namespace paro {
 
 // Opts kernel Kern into `bytes` of dynamic shared memory on the current
-// device, once for each size that grows (the attribute outlives the call;
-// setting it every time is a microsecond of a small call).
-template <auto Kern>
+// device (kClusters: and into clusters of more than 8 CTAs), once for each
+// size that grows: the attribute outlives the call, and setting it every
+// time is a microsecond of a small call.
+template <auto Kern, bool kClusters = false>
 cudaError_t opt_in_smem(int bytes) {
   constexpr int kDevices = 64;
   static std::atomic<int> done[kDevices];
@@ -20,6 +21,8 @@ cudaError_t opt_in_smem(int bytes) {
   if (e != cudaSuccess) return e;
   if (dev < kDevices && done[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (kClusters && e == cudaSuccess)
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < kDevices) done[dev].store(bytes, std::memory_order_relaxed);
   return e;
 }

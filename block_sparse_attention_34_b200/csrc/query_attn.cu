@@ -839,9 +839,7 @@ cudaError_t launch_units(const void* q, const void* k, const void* v, const floa
                          const int32_t* lengths, void* out, int32_t* idx, float* lse,
                          int32_t* status, cudaStream_t s) {
   auto kern = query_attn_kernel<T, D, kUnits>;
-  cudaError_t e = opt_in_smem<query_attn_kernel<T, D, kUnits>>(smem);
-  if (e == cudaSuccess && C > 8)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const cudaError_t e = opt_in_smem<query_attn_kernel<T, D, kUnits>, true>(smem);
   if (e != cudaSuccess) return e;
   const int tiles = (per_head + R - 1) / R;
   cudaLaunchConfig_t cfg = {};

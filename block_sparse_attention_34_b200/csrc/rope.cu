@@ -251,7 +251,7 @@ struct Unit {
 };
 
 // x -> y, any strides of batch, head and token.  A thread owns one unit of
-// one token and goes over kHeads heads with it: the table is read once for
+// one token and goes over `per` heads with it, at most kHeads: the table is read once for
 // them, and all their loads are in flight before the first store.  Rows of
 // 16 (or 32) tokens of a head are neighbours in a head-major tensor, rows of
 // kHeads heads of a token in a token-major one: both sides move whole
@@ -260,7 +260,7 @@ struct Unit {
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kThreads)
     rope_kernel(const T* x, RowStride xs, T* y, RowStride ys, int N, int H, int W, int heads,
-                const __grid_constant__ RopeTab tab, const float* __restrict__ table,
+                int per, const __grid_constant__ RopeTab tab, const float* __restrict__ table,
                 const int32_t* __restrict__ positions, int64_t pos_batch, float sign,
                 int32_t* __restrict__ status) {
   using U = Unit<T, kInter>;
@@ -290,13 +290,13 @@ __global__ void __launch_bounds__(kThreads)
     pos[1] = n / W % H;
     pos[2] = n % W;
   }
-  const int h0 = blockIdx.y * kHeads;
+  const int h0 = blockIdx.y * per, mine = min(per, heads - h0);  // this CTA's heads
   const T* src = x + b * xs.batch + h0 * xs.head + (int64_t)n * xs.token + c * U::E;
   T* dst = y + b * ys.batch + h0 * ys.head + (int64_t)n * ys.token + c * U::E;
   U unit[kHeads];
 #pragma unroll
   for (int h = 0; h < kHeads; ++h)
-    if (h0 + h < heads)
+    if (h < mine)
 #pragma unroll
       for (int k = 0; k < U::kChunks; ++k)
         unit[h].u[k] = load_once(src + h * xs.head + k * (D / 2));
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 #pragma unroll
   for (int h = 0; h < kHeads; ++h)
-    if (h0 + h < heads) {
+    if (h < mine) {
       float2 a[U::kTwo], b2[U::kTwo];
       unit[h].unpack(a, b2);
       U::rotate(a, b2, cos[0], sin[0], nsin);
@@ -477,9 +477,10 @@ cudaError_t launch_rope_typed(const void* x, RowStride xs, void* y, RowStride ys
   using U = Unit<T, kInter>;
   constexpr int kTokens = kThreads / (D / U::E / U::kChunks);
   constexpr int kHeads = 8 / U::kChunks;
-  const dim3 grid((g.N + kTokens - 1) / kTokens, (g.heads + kHeads - 1) / kHeads, g.B);
+  const int groups = (g.heads + kHeads - 1) / kHeads, per = (g.heads + groups - 1) / groups;
+  const dim3 grid((g.N + kTokens - 1) / kTokens, (g.heads + per - 1) / per, g.B);
   rope_kernel<T, D, kInter><<<grid, kThreads, 0, s>>>(
-      static_cast<const T*>(x), xs, static_cast<T*>(y), ys, g.N, g.H, g.W, g.heads, tab,
+      static_cast<const T*>(x), xs, static_cast<T*>(y), ys, g.N, g.H, g.W, g.heads, per, tab,
       table, positions, pos_batch, inverse ? -1.f : 1.f, status);
   return cudaGetLastError();
 }

@@ -238,9 +238,9 @@ def reorder(x, pr: Problem, out=None, pool=None, with_pool=False):
         raise ValueError(f"x: {tuple(x.shape)} {x.dtype}, expected {pr.natural} and one of {_FLOAT}")
     _expect(out, "out", pr.permuted, x.dtype)
     _expect(pool, "pool", pr.pooled, torch.float32)
-    out = out if out is not None else torch.empty(pr.permuted, dtype=x.dtype, device=x.device)
+    out = out if out is not None else x.new_empty(pr.permuted)
     if with_pool and pool is None:
-        pool = torch.empty(pr.pooled, dtype=torch.float32, device=x.device)
+        pool = x.new_empty(pr.pooled, dtype=torch.float32)
     _launch(x, load().pa_reorder, x.data_ptr(), out.data_ptr(), _dtype_code(x), pr.shape,
             pr.perms_ptr, _addr(pool))
     return (out, pool) if (with_pool or pool is not None) else out
@@ -550,19 +550,39 @@ def _launch(t, fn, *args):
         raise ParoError(status, load().pa_last_error().decode())
 
 
-def _same_device(t, *named):
-    """Raise ValueError unless the tensors given are contiguous and on the
-    device of ``t``."""
+def _device_of(t):
     i = t.get_device()
     if i < 0:
         raise ValueError("tensors must be on a CUDA device (no CPU path)")
-    for name, u in named:
-        if u is None:
-            continue
-        if u is not t and u.get_device() != i:
-            raise ValueError(f"{name}: on {u.device}, expected {t.device}")
-        if not u.is_contiguous():
-            raise ValueError(f"{name}: tensors must be contiguous")
+    return i
+
+
+def _need(i, name, t, shape, dtype):
+    """Raise ValueError unless ``t`` is contiguous, on device ``i``, and of
+    that shape and type: the library reads and writes whole buffers of the
+    sizes the problem implies."""
+    if t.get_device() == i and t.shape == shape and t.dtype == dtype and t.is_contiguous():
+        return
+    if t.get_device() != i:
+        raise ValueError(f"{name}: on {t.device}, expected device {i}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
+
+
+def _need_status(i, status):
+    if status is not None:
+        _need(i, "status", status, status.shape, torch.int32)
+        _expect_status(status)
+
+
+def _need_lists(i, idx, counts, pr):
+    """idx [B,h,NB,k_max] int32 with 0 <= k_max <= NB; counts [B,h,NB] int32."""
+    if idx.dim() != 4 or idx.shape[3] > pr.NB:
+        raise ValueError(f"idx: shape {tuple(idx.shape)}, expected {pr.per_block + ('k<=NB',)}")
+    _need(i, "idx", idx, pr.per_block + (idx.shape[3],), torch.int32)
+    if counts is not None:
+        _need(i, "counts", counts, pr.per_block, torch.int32)
 
 
 def _addr(t):
@@ -630,13 +650,13 @@ def _row_strides(t, name):
 
 
 def _rope_checks(x, rope, d):
-    if x.get_device() < 0:
-        raise ValueError("tensors must be on a CUDA device (no CPU path)")
+    i = _device_of(x)
     if x.dim() != 4 or x.dtype not in _FLOAT or x.numel() == 0:
         raise ValueError(f"x: [B, heads, N, d] of float32 or bfloat16, got {tuple(x.shape)} {x.dtype}")
-    if rope.d != d or x.shape[3] != d or rope.table.get_device() != x.get_device():
+    if rope.d != d or x.shape[3] != d or rope.table.get_device() != i:
         raise ValueError(f"rope: a table for d = {rope.d} on {rope.table.device}, x has d = {x.shape[3]} "
                          f"on {x.device}")
+    return i
 
 
 def _dense_rows(t):
@@ -662,8 +682,7 @@ def rope3d(x, rope: RopeTable, positions=None, inverse=False, out=None, status=N
     back: the gradient's rotation.  ``out``: any non-overlapping strides, or
     x itself (not a tensor that shares only part of x's memory); contiguous
     by default."""
-    _rope_checks(x, rope, rope.d)
-    _same_device(x, ("positions", positions), ("status", status))
+    i = _rope_checks(x, rope, rope.d)
     B, heads, N, d = x.shape
     if positions is None:
         F, H, W = rope.extent if grid is None else grid
@@ -675,18 +694,16 @@ def rope3d(x, rope: RopeTable, positions=None, inverse=False, out=None, status=N
             raise ValueError("grid or positions, not both")
         F, H, W = 1, 1, N
         batched = int(positions.dim() == 3)
-        if positions.shape != ((B, N, 3) if batched else (N, 3)) or positions.dtype != torch.int32:
-            raise ValueError(f"positions: {tuple(positions.shape)} {positions.dtype}, expected int32 "
-                             f"({N}, 3) or ({B}, {N}, 3)")
-    _expect_status(status)
+        _need(i, "positions", positions, (B, N, 3) if batched else (N, 3), torch.int32)
+    _need_status(i, status)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
         out_strides = None
     else:
         _expect(out, "out", x.shape, x.dtype)
-        if out.get_device() != x.get_device():
+        if out.get_device() != i:
             raise ValueError(f"out: on {out.device}, x is on {x.device}")
-        if not _dense_rows(out):
+        if not (out.is_contiguous() or _dense_rows(out)):
             raise ValueError("out: rows overlap")
         out_strides = _row_strides(out, "out")
     _launch(x, load().pa_rope_apply, x.data_ptr(), _row_strides(x, "x"), out.data_ptr(), out_strides,
@@ -701,27 +718,22 @@ def rope_reorder(x, rope: RopeTable, pr: Problem, out=None, pool=None, with_pool
     ``pool``), the block means of the rotated rows (taken before they are
     rounded): returns (x_perm, pool).  x as for :func:`rope3d`, token n at
     its place in pr's grid, which ``rope.extent`` has to cover."""
-    _rope_checks(x, rope, pr.d)
-    _same_device(x, ("out", out), ("pool", pool))
+    i = _rope_checks(x, rope, pr.d)
     if x.shape != pr.natural:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected {pr.natural}")
     if rope.extent[0] < pr.F or rope.extent[1] < pr.H or rope.extent[2] < pr.W:
         raise ValueError(f"rope.extent {rope.extent} does not cover the grid {(pr.F, pr.H, pr.W)}")
-    _expect(out, "out", pr.permuted, x.dtype)
-    _expect(pool, "pool", pr.pooled, torch.float32)
     if out is None:
-        out = torch.empty(pr.permuted, dtype=x.dtype, device=x.device)
-    if with_pool and pool is None:
-        pool = torch.empty(pr.pooled, dtype=torch.float32, device=x.device)
+        out = x.new_empty(pr.permuted)
+    else:
+        _need(i, "out", out, pr.permuted, x.dtype)
+    if pool is not None:
+        _need(i, "pool", pool, pr.pooled, torch.float32)
+    elif with_pool:
+        pool = x.new_empty(pr.pooled, dtype=torch.float32)
     _launch(x, load().pa_rope_reorder, x.data_ptr(), _row_strides(x, "x"), out.data_ptr(),
             _dtype_code(x), pr.shape, pr.perms_ptr, rope.desc, rope.table.data_ptr(), _addr(pool))
     return (out, pool) if pool is not None else out
-
-
-def _bf16(shape, *named):
-    for name, t in named:
-        if t is not None and (t.shape != shape or t.dtype != torch.bfloat16):
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {shape} torch.bfloat16")
 
 
 def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=None, status=None):
@@ -729,15 +741,19 @@ def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=
     [B, heads, N_p, d] (:func:`reorder` or :func:`rope_reorder`), which also
     returns the natural log-sum-exp of every row, [B, heads, N] float32 (-inf
     for a row without kept blocks): the forward pass of training."""
-    _same_device(q, ("q", q), ("k", k), ("v", v), ("idx", idx), ("counts", counts), ("out", out),
-                 ("lse", lse), ("status", status))
-    _bf16(pr.permuted, ("q", q), ("k", k), ("v", v))
-    _check_lists(idx, counts, pr)
-    _expect(out, "out", pr.natural, torch.bfloat16)
-    _expect(lse, "lse", pr.rows, torch.float32)
-    _expect_status(status)
-    out = out if out is not None else torch.empty(pr.natural, dtype=torch.bfloat16, device=q.device)
-    lse = lse if lse is not None else torch.empty(pr.rows, dtype=torch.float32, device=q.device)
+    i = _device_of(q)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need(i, name, t, pr.permuted, torch.bfloat16)
+    _need_lists(i, idx, counts, pr)
+    _need_status(i, status)
+    if out is None:
+        out = q.new_empty(pr.natural)
+    else:
+        _need(i, "out", out, pr.natural, torch.bfloat16)
+    if lse is None:
+        lse = q.new_empty(pr.rows, dtype=torch.float32)
+    else:
+        _need(i, "lse", lse, pr.rows, torch.float32)
     _launch(q, load().pa_block_sparse_attn_lse, q.data_ptr(), k.data_ptr(), v.data_ptr(), PA_BF16,
             pr.shape, pr.perms_ptr, _addr(idx), _addr(counts), idx.shape[3], out.data_ptr(), lse.data_ptr(), _addr(status))
     return out, lse
@@ -751,20 +767,26 @@ def block_sparse_attn_backward(dout, q, k, v, out, lse, pr: Problem, idx, counts
     used.  The same bits on every run.  ``workspace``: a uint8 tensor of at
     least :func:`backward_workspace` bytes that no call in flight uses (by
     default allocated here)."""
-    _same_device(q, ("q", q), ("k", k), ("v", v), ("dout", dout), ("out", out), ("lse", lse),
-                 ("idx", idx), ("counts", counts), ("dlse", dlse), ("dq", dq), ("dk", dk), ("dv", dv),
-                 ("workspace", workspace), ("status", status))
-    _bf16(pr.permuted, ("q", q), ("k", k), ("v", v))
-    _bf16(pr.natural, ("dout", dout), ("out", out), ("dq", dq), ("dk", dk), ("dv", dv))
-    for name, t in (("lse", lse), ("dlse", dlse)):
-        _expect(t, name, pr.rows, torch.float32)
-    _check_lists(idx, counts, pr)
-    _expect_status(status)
-    dq, dk, dv = (t if t is not None else torch.empty_like(out) for t in (dq, dk, dv))
+    i = _device_of(q)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need(i, name, t, pr.permuted, torch.bfloat16)
+    _need(i, "dout", dout, pr.natural, torch.bfloat16)
+    _need(i, "out", out, pr.natural, torch.bfloat16)
+    _need(i, "lse", lse, pr.rows, torch.float32)
+    if dlse is not None:
+        _need(i, "dlse", dlse, pr.rows, torch.float32)
+    _need_lists(i, idx, counts, pr)
+    _need_status(i, status)
+    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        if t is not None:
+            _need(i, name, t, pr.natural, torch.bfloat16)
+    dq = torch.empty_like(out) if dq is None else dq
+    dk = torch.empty_like(out) if dk is None else dk
+    dv = torch.empty_like(out) if dv is None else dv
     if workspace is None:
-        workspace = torch.empty(backward_workspace(pr), dtype=torch.uint8, device=q.device)
-    elif workspace.dtype != torch.uint8:
-        raise ValueError(f"workspace: dtype {workspace.dtype}, expected torch.uint8")
+        workspace = q.new_empty(backward_workspace(pr), dtype=torch.uint8)
+    else:
+        _need(i, "workspace", workspace, workspace.shape, torch.uint8)
     _launch(q, load().pa_block_sparse_attn_backward, dout.data_ptr(), q.data_ptr(), k.data_ptr(),
             v.data_ptr(), out.data_ptr(), lse.data_ptr(), _addr(dlse), PA_BF16, pr.shape,
             pr.perms_ptr, _addr(idx), _addr(counts), idx.shape[3], dq.data_ptr(), dk.data_ptr(),
@@ -796,32 +818,37 @@ def block_sparse_query_attn(q, k, v, k_pool, pr: Problem, k_keep: int, lengths=N
     bfloat16.  Returns (out [B, q_heads, M, d], idx [B, q_heads, M, k_keep]
     ascending with -1 behind the last, lse [B, q_heads, M]); a row without
     keys gives zeros and -inf."""
-    _same_device(q, ("q", q), ("k", k), ("v", v), ("k_pool", k_pool), ("lengths", lengths),
-                 ("out", out), ("idx", idx), ("lse", lse), ("status", status))
-    if q.dim() != 4 or q.shape[0] != pr.B or q.shape[1] % pr.heads or q.shape[3] != pr.d or q.numel() == 0:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected ({pr.B}, a multiple of {pr.heads}, M, {pr.d})")
-    if q.dtype not in _FLOAT:
-        raise ValueError(f"q: dtype {q.dtype}, expected one of {_FLOAT}")
-    for name, t in (("k", k), ("v", v)):
-        if t.shape != pr.permuted or t.dtype != q.dtype:
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected {pr.permuted} {q.dtype}")
-    if k_pool.shape != pr.pooled or k_pool.dtype != torch.float32:
-        raise ValueError(f"k_pool: {tuple(k_pool.shape)} {k_pool.dtype}, expected {pr.pooled} torch.float32")
-    _expect(lengths, "lengths", (pr.B,), torch.int32)
-    rows = tuple(q.shape[:3])
-    _expect(out, "out", q.shape, q.dtype)
-    _expect(idx, "idx", rows + (int(k_keep),), torch.int32)
-    _expect(lse, "lse", rows, torch.float32)
-    _expect_status(status)
+    i = _device_of(q)
+    if q.dim() != 4 or q.dtype not in _FLOAT:
+        raise ValueError(f"q: {tuple(q.shape)} {q.dtype}, expected four dimensions and one of {_FLOAT}")
+    B, heads, M, d = q.shape
+    if B != pr.B or heads < 1 or heads % pr.heads or M < 1 or d != pr.d or not q.is_contiguous():
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected ({pr.B}, a multiple of {pr.heads}, M, {pr.d}) "
+                         "and contiguous")
+    k_keep = int(k_keep)
     if not 1 <= k_keep <= pr.NB:
         raise ValueError(f"k_keep={k_keep} must be in [1, {pr.NB}]")
-    dev = q.device
-    out = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=dev)
-    idx = idx if idx is not None else torch.empty(rows + (int(k_keep),), dtype=torch.int32, device=dev)
-    lse = lse if lse is not None else torch.empty(rows, dtype=torch.float32, device=dev)
+    _need(i, "k", k, pr.permuted, q.dtype)
+    _need(i, "v", v, pr.permuted, q.dtype)
+    _need(i, "k_pool", k_pool, pr.pooled, torch.float32)
+    if lengths is not None:
+        _need(i, "lengths", lengths, (B,), torch.int32)
+    _need_status(i, status)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(i, "out", out, q.shape, q.dtype)
+    if idx is None:
+        idx = q.new_empty((B, heads, M, k_keep), dtype=torch.int32)
+    else:
+        _need(i, "idx", idx, (B, heads, M, k_keep), torch.int32)
+    if lse is None:
+        lse = q.new_empty((B, heads, M), dtype=torch.float32)
+    else:
+        _need(i, "lse", lse, (B, heads, M), torch.float32)
     _launch(q, load().pa_query_attn, q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pool.data_ptr(),
-            _dtype_code(q), pr.shape, q.shape[1] // pr.heads, q.shape[2], int(k_keep),
-            _addr(lengths), out.data_ptr(), idx.data_ptr(), lse.data_ptr(), _addr(status))
+            _dtype_code(q), pr.shape, heads // pr.heads, M, k_keep, _addr(lengths),
+            out.data_ptr(), idx.data_ptr(), lse.data_ptr(), _addr(status))
     return out, idx, lse
 
 

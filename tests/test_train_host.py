@@ -162,7 +162,7 @@ def test_the_binding_refuses_host_tensors_and_wrong_shapes(lib):
 def device_blind(monkeypatch):
     """The binding's checks of shapes and types alone, on host tensors; the
     library must not be reached."""
-    monkeypatch.setattr(paro, "_same_device", lambda t, *named: None)
+    monkeypatch.setattr(paro, "_device_of", lambda t: t.get_device())
     monkeypatch.setattr(paro, "_launch", lambda *a: pytest.fail("the call reached the library"))
 
 
