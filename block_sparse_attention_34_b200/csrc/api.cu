@@ -662,9 +662,10 @@ pa_status pa_block_sparse_attn_lse(const void* q, const void* k, const void* v, 
 
 namespace {
 // The backward pass's workspace: dO permuted, row statistics, transposed
-// kept lists, each at a multiple of 256 bytes.
+// kept lists, their checked lengths, the counters of blocks handed out, each
+// at a multiple of 256 bytes.
 struct BwdLayout {
-  int64_t nlse, ndel, mask, bytes;
+  int64_t nlse, ndel, mask, checked, counters, bytes;
   int words;
 };
 BwdLayout bwd_layout(const paro::Grid& g) {
@@ -675,7 +676,10 @@ BwdLayout bwd_layout(const paro::Grid& g) {
   l.nlse = up(rows * g.d * 2);
   l.ndel = l.nlse + up(rows * 4);
   l.mask = l.ndel + up(rows * 4);
-  l.bytes = l.mask + up((int64_t)g.B * g.heads * g.NB * l.words * 4);
+  const int64_t lists = (int64_t)g.B * g.heads * g.NB;
+  l.checked = l.mask + up(lists * l.words * 4);
+  l.counters = l.checked + up(lists * 4);
+  l.bytes = l.counters + 256;
   return l;
 }
 }  // namespace
@@ -720,6 +724,8 @@ pa_status pa_block_sparse_attn_backward(const void* dout, const void* q, const v
   a.nlse = reinterpret_cast<float*>(w + l.nlse);
   a.ndel = reinterpret_cast<float*>(w + l.ndel);
   a.mask = reinterpret_cast<uint32_t*>(w + l.mask);
+  a.checked = reinterpret_cast<int32_t*>(w + l.checked);
+  a.counters = reinterpret_cast<int32_t*>(w + l.counters);
   a.words = l.words;
   a.idx = idx;
   a.counts = counts;

@@ -31,8 +31,8 @@ constexpr int kBits = 4096;  // key blocks whose bits a CTA collects at a time
 
 // CTAs x < words: 32 query blocks' kept lists of one head (a warp a list, in
 // turn) -> word x of every key block's row of the transposed mask, collected
-// in shared memory, so the mask needs no clearing.  A malformed list is
-// reported and sets nothing.  The other CTAs: a group of d/8 lanes per
+// in shared memory, so the mask needs no clearing, and how many entries each
+// list has (-1: malformed, which is reported and sets nothing).  The other CTAs: a group of d/8 lanes per
 // permuted row reads O and dO at the row's natural position (16 bytes a
 // lane), writes dO permuted and the row's statistics; bound by HBM, two
 // reads and a write of the tensor (480p, 12 heads: 56 us, 5.4 TB/s).
@@ -44,8 +44,10 @@ __global__ void __launch_bounds__(kThreads)
                     const int32_t* __restrict__ counts, int k_max, int words,
                     __nv_bfloat16* __restrict__ dop, float* __restrict__ nlse,
                     float* __restrict__ ndel, uint32_t* __restrict__ mask,
+                    int32_t* __restrict__ checked, int32_t* __restrict__ counters,
                     int32_t* __restrict__ status) {
   const int64_t bh = blockIdx.y;
+  if (blockIdx.x == 0 && bh == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0;
   if ((int)blockIdx.x < words) {
     __shared__ uint32_t bits[kBits];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -58,10 +60,12 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t row = bh * g.NB + i;
         const int cnt = counts != nullptr ? __ldg(counts + row) : k_max;
         const int32_t* ids = idx + row * k_max;
-        if (!list_ok(ids, cnt, k_max, g.NB, lane)) {
-          if (lane == 0) report(status, PA_ERR_DEVICE_CHECK);
-          continue;
+        const bool fine = list_ok(ids, cnt, k_max, g.NB, lane);
+        if (lane == 0) {
+          checked[row] = fine ? cnt : -1;
+          if (!fine) report(status, PA_ERR_DEVICE_CHECK);
         }
+        if (!fine) continue;
         for (int e = lane; e < cnt; e += 32) {
           const int j = __ldg(ids + e) - j0;
           if (j >= 0 && j < n) atomicOr(bits + j, 1u << (i & 31));
@@ -111,7 +115,7 @@ cudaError_t launch_bwd_prep(const void* out, const void* dout, const float* lse,
   auto* d = static_cast<const __nv_bfloat16*>(dout);
   auto kern = g.d == 64 ? bwd_prep_kernel<64> : bwd_prep_kernel<128>;
   kern<<<grid, kThreads, 0, s>>>(o, d, lse, dlse, g, a.idx, a.counts, a.k_max, a.words, a.dop, a.nlse,
-                                 a.ndel, a.mask, a.status);
+                                 a.ndel, a.mask, a.checked, a.counters, a.status);
   return cudaGetLastError();
 }
 

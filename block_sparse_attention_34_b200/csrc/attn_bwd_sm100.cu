@@ -16,14 +16,23 @@
 // value crosses a thread: lse and D come with the row (dQ) or, from shared
 // memory, with the column (dK, dV).
 //
+// The grid is one CTA per SM, which takes the key blocks, then the query
+// blocks, from a counter each: a block's loads start while the last one's
+// sums are stored, and its first products follow the last one's without a
+// pause.  (A CTA per block, which starts and ends 7 us around its tiles,
+// took 299 us for the two clips of 12 tiles a block, this form 250 us.)
+//
 // 12 warps:
 //   0-7    elementwise; warp w holds lanes 32 (w % 4) .. +31 (a row a
 //          thread) and the tile's columns 64 (w / 4) .. +63, so that two
 //          warps share each scheduler and the exponentials of one hide the
-//          tensor-memory loads of the other;
+//          tensor-memory loads of the other; at a block's end they read its
+//          sums and store them;
 //   8      tensor memory, and one lane that issues every MMA;
 //   9, 10  TMA loads of A1, A2, B1 and of B2;
-//   11     checks the kept list (dQ).
+//   11     takes the blocks and hands them to the other warps, two ahead.
+// The tiles of a CTA's blocks are numbered through (T below): stages and
+// barrier phases go on from block to block.
 // Tensor memory, 512 columns: kKeys X 0, Y 128, G1 256, G2 384; dQ X0 0,
 // X1 128, Y 256, G1 384.  A thread writes its P (or dS) as bf16 pairs over
 // the columns of X (or Y) that it read itself: 32 columns from column 64 g
@@ -47,32 +56,39 @@ namespace {
 using namespace sm100;
 
 constexpr int kBlock = 128;
-constexpr int kMmaWarp = 8, kB1Warp = 9, kB2Warp = 10, kCheckWarp = 11;
+constexpr int kSms = 148;
+constexpr int kMmaWarp = 8, kB1Warp = 9, kB2Warp = 10, kItemWarp = 11;
 constexpr int kThreads = 12 * 32;
 constexpr int kAluThreads = 256;
 constexpr uint32_t kHalf = kBlock * 128;  // 64 columns of a tile: 16 KB
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kOffBar = 0;
-constexpr uint32_t kOffSlot = 256;
-constexpr uint32_t kOffStats = 512;  // kKeys: [2 stages][-lse, -D][128] float
+constexpr uint32_t kOffBar = 0;      // two sets of NBAR barriers: kKeys, dQ
+constexpr uint32_t kOffSlot = 512;   // tensor memory's base, the abort flag
+constexpr uint32_t kOffItems = 528;  // [2 sets][2] of (block of the grid, tiles)
+constexpr uint32_t kOffStats = 1024;  // kKeys: [2 stages][-lse, -D][128] float
 constexpr uint32_t kStatBytes = kBlock * 4;
 constexpr uint32_t kSmall = 3072;  // operand tiles from here, 1024-aligned
 
 enum : uint32_t {
-  BA = 0,     // A1, A2 loaded
-  BB1 = 1,    // B1 stage full (3)
-  BB2 = 4,    // B2 stage full (2)
-  BX = 6,     // X(t) complete (ring of 2)
-  BY = 8,     // Y(t) complete (ring of 2)
-  BG1 = 10,   // G1(t) complete: its B1 stage is free (3)
-  BG2 = 13,   // G2(t) complete: its B2 stage is free (2)
-  BP = 15,    // P(t) written by every elementwise thread
-  BS = 16,    // dS(t) written
-  BDRAIN = 17,
-  NBAR = 18
+  BA = 0,      // A1, A2 of the block loaded
+  BB1 = 1,     // B1 stage full (3)
+  BB2 = 4,     // B2 stage full (2)
+  BX = 6,      // X(T) complete (ring of 2)
+  BY = 8,      // Y(T) complete (ring of 2)
+  BG1 = 10,    // G1(T) complete: its B1 stage is free (3)
+  BG2 = 13,    // G2(T) complete: its B2 stage is free (2)
+  BP = 15,     // P(T) written by every elementwise thread
+  BS = 16,     // dS(T) written
+  BFREE = 17,  // the block's sums read by every elementwise thread
+  BAFREE = 18,  // the block's last product that reads A1 or A2 (Y) complete
+  BDRAIN = 19,
+  BITEM = 20,   // a block handed out (ring of 2)
+  BTAKEN = 22,  // and taken by every warp (2)
+  NBAR = 24
 };
-static_assert(NBAR * 8 <= kOffSlot, "barrier region");
+static_assert(2 * NBAR * 8 <= kOffSlot, "barrier region");
 static_assert(kOffStats + 4 * kStatBytes <= kSmall, "statistics region");
+constexpr uint32_t kTakers = 8 + 2 + 1;  // elementwise warps, loaders, MMA
 
 template <bool kKeys>
 constexpr int kB1Stages = kKeys ? 2 : 3;
@@ -88,112 +104,111 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// All blocks of one use that this CTA takes.  Returns with none of its
+// copies or MMAs in flight, whatever happened.
 template <bool kKeys, int D>
-__device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUtensorMap& map_a2,
-                                          const CUtensorMap& map_b1, const CUtensorMap& map_b2,
-                                          const BwdArgs& args, const Grid& g, float scale,
-                                          float scale_log2) {
-  const float* __restrict__ nlse = args.nlse;
-  const float* __restrict__ ndel = args.ndel;
-  const int words = args.words, k_max = args.k_max;
-  const int32_t *idx = args.idx, *counts = args.counts;
-  const uint32_t* __restrict__ mask = args.mask;
-  __nv_bfloat16* __restrict__ g1 = kKeys ? args.dk : args.dq;
-  __nv_bfloat16* __restrict__ g2 = args.dv;  // kKeys only
-  int32_t* status = args.status;
+__device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUtensorMap& map_a2,
+                                           const CUtensorMap& map_b1, const CUtensorMap& map_b2,
+                                           const BwdArgs& args, const Grid& g, float scale,
+                                           float scale_log2, unsigned char* smem, uint32_t base,
+                                           uint32_t tmem, Ctl ctl) {
   constexpr uint32_t kTile = kBlock * D * 2;
   constexpr int kS1 = kB1Stages<kKeys>;
   constexpr uint32_t kOffA1 = kSmall, kOffA2 = kOffA1 + kTile, kOffB1 = kOffA2 + kTile,
                      kOffB2 = kOffB1 + kS1 * kTile;
   constexpr uint32_t kColX = 0, kColY = kKeys ? 128 : 256, kColG1 = kKeys ? 256 : 384,
                      kColG2 = 384;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  const uint32_t base = smem_u32(smem_raw);
-  if ((base & 1023u) != 0) {
-    if (threadIdx.x == 0) report(status, PA_ERR_UNSUPPORTED);
-    return;
-  }
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + kOffSlot);
-  volatile uint32_t* abort_flag = tmem_slot + 1;
-  volatile uint32_t* bad_flag = tmem_slot + 2;
-  auto bar = [&](uint32_t slot) { return base + kOffBar + slot * 8u; };
-
+  auto bar = [&](uint32_t slot) {
+    return base + kOffBar + ((kKeys ? 0u : (uint32_t)NBAR) + slot) * 8u;
+  };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int blk = blockIdx.x;  // this CTA's block of rows
-  const int64_t bh = blockIdx.y;
-  const int order = g.perm[(int)(bh % g.heads)];
-  const int64_t row = bh * g.NB + blk;
-  const int row0 = (int)(bh * g.Np);  // first row of the head
-  const int32_t* ids = kKeys ? nullptr : idx + row * k_max;
-  const uint32_t* bits = kKeys ? mask + row * words : nullptr;
-  const Ctl ctl{abort_flag, status, kTimeoutNs};
-  const bool expired =
-      status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT;
+  const int64_t rows = (int64_t)g.B * g.heads * g.NB;
+  volatile int32_t* items = reinterpret_cast<int32_t*>(smem + kOffItems) + (kKeys ? 0 : 4);
+  const int words = args.words;
 
-  // tiles of the list: kKeys counts the bits of the row of the mask
-  int cnt;
-  if constexpr (kKeys) {
-    cnt = 0;
-    for (int w = lane; w < words; w += 32) cnt += __popc(__ldg(bits + w));
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
-  } else {
-    cnt = counts != nullptr ? __ldg(counts + row) : k_max;
-  }
+  // The next block handed out: its row of the grid (< 0: none is left, or a
+  // wait ran out) and its tiles (< 0: a malformed list).  One warp.
+  int handed = 0;
+  auto take = [&](int& n) -> int {
+    const int s = handed & 1;
+    if (!all_wait(bar(BITEM + s), (handed >> 1) & 1, ctl)) return -1;
+    const int row = items[2 * s];
+    n = items[2 * s + 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(BTAKEN + s));
+    ++handed;
+    return row;
+  };
 
-  if (threadIdx.x == 0) {
-    mbar_init(bar(BA), 1);
-    for (int s = 0; s < 3; ++s) {
-      mbar_init(bar(BB1 + s), 1);
-      mbar_init(bar(BG1 + s), 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(BB2 + s), 1);
-      mbar_init(bar(BX + s), 1);
-      mbar_init(bar(BY + s), 1);
-      mbar_init(bar(BG2 + s), 1);
-    }
-    mbar_init(bar(BP), kAluThreads);
-    mbar_init(bar(BS), kAluThreads);
-    mbar_init(bar(BDRAIN), 1);
-    *abort_flag = 0;
-    *bad_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-  }
-  if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-  if (!kKeys && warp == kCheckWarp && !list_ok(ids, cnt, k_max, g.NB, lane) && lane == 0) {
-    *bad_flag = 1;
-    report(status, PA_ERR_DEVICE_CHECK);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const bool run = *bad_flag == 0 && !expired;
-  const int n = run ? cnt : 0;
-
-  if (warp >= 8) {
-    if ((warp == kB1Warp || warp == kB2Warp) && n > 0) {
-      // ---------------------------------------------------- copies ----
-      const bool first = warp == kB1Warp;
-      const int stages = first ? kS1 : kB2Stages;
-      const uint32_t ring = base + (first ? kOffB1 : kOffB2);
-      const CUtensorMap* map = first ? &map_b1 : &map_b2;
-      // a stage is free once the last product that reads it completed: B1's
-      // is G1; B2's is G2, or Y where there is no G2
-      const uint32_t full0 = first ? BB1 : BB2, free0 = first ? BG1 : kKeys ? BG2 : BY;
-      if (first && lane == 0) {
+  int n = 0;
+  uint32_t T = 0;     // tiles of the blocks before this one
+  uint32_t full = 0;  // blocks with tiles before this one
+  if (warp == kItemWarp) {
+    // -------------------------------------------------------- blocks ----
+    // Hands out a block, then loads its A1, A2 once the last block's products
+    // have read theirs: a block is known to the other warps, and its first
+    // column tiles are on their way, while the one before it is worked on.
+    for (int i = 0;; ++i) {
+      const int s = i & 1;
+      if (i >= 2 && !warp_wait(bar(BTAKEN + s), ((i >> 1) - 1) & 1, ctl)) break;
+      int row = 0;
+      if (lane == 0) row = atomicAdd(args.counters + (kKeys ? 0 : 1), 1);
+      row = __shfl_sync(0xffffffffu, row, 0);
+      int cnt = 0;
+      if (row < rows) {
+        if constexpr (kKeys) {
+          const uint32_t* bits = args.mask + (int64_t)row * words;
+          for (int w = lane; w < words; w += 32) cnt += __popc(__ldg(bits + w));
+          cnt = __reduce_add_sync(0xffffffffu, cnt);
+        } else {
+          cnt = __ldg(args.checked + row);
+        }
+      } else {
+        row = -1;
+      }
+      if (lane == 0) {
+        items[2 * s] = row;
+        items[2 * s + 1] = cnt;
+        mbar_arrive(bar(BITEM + s));  // release: the stores above are visible to the takers
+      }
+      if (row < 0) break;
+      if (cnt <= 0) continue;
+      if (full > 0 && !warp_wait(bar(BAFREE), (full - 1) & 1, ctl)) break;
+      if (lane == 0) {
+        const int bh = row / g.NB, at = bh * g.Np + (row - bh * g.NB) * kBlock;
         mbar_arrive_tx(bar(BA), 2 * kTile);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-          tma_load_2d(base + kOffA1 + h * kHalf, &map_a1, 64 * h, row0 + blk * kBlock, bar(BA));
-          tma_load_2d(base + kOffA2 + h * kHalf, &map_a2, 64 * h, row0 + blk * kBlock, bar(BA));
+          tma_load_2d(base + kOffA1 + h * kHalf, &map_a1, 64 * h, at, bar(BA));
+          tma_load_2d(base + kOffA2 + h * kHalf, &map_a2, 64 * h, at, bar(BA));
         }
       }
-      int issued = 0;
-      int word = -1;          // kKeys: the current word of the mask
+      ++full;
+    }
+    // on every path this warp's copies have landed before it leaves
+    if (lane == 0 && full > 0) drain_phase(bar(BA), (full - 1) & 1);
+    __syncwarp();
+  } else if (warp == kB1Warp || warp == kB2Warp) {
+    // -------------------------------------------------------- copies ----
+    const bool first = warp == kB1Warp;
+    const int stages = first ? kS1 : kB2Stages;
+    const uint32_t ring = base + (first ? kOffB1 : kOffB2);
+    const CUtensorMap* map = first ? &map_b1 : &map_b2;
+    // a stage is free once the last product that reads it completed: B1's
+    // is G1; B2's is G2, or Y where there is no G2
+    const uint32_t full0 = first ? BB1 : BB2, free0 = first ? BG1 : kKeys ? BG2 : BY;
+    uint32_t issued = 0;  // tiles copied
+    for (bool ok = true; ok;) {
+      const int row = take(n);
+      if (row < 0) break;
+      if (n <= 0) continue;
+      const int row0 = row / g.NB * g.Np;  // first row of the head
+      const uint32_t* bits = args.mask + (int64_t)row * words;
+      const int32_t* ids = args.idx + (int64_t)row * args.k_max;
+      int word = -1;                 // kKeys: the current word of the mask
       uint32_t left = 0, chunk = 0;  // its bits left; words 32 (word / 32) + lane
-      int id_lane = 0;        // dQ: entry 32 (t / 32) + lane
-      for (int t = 0; t < n; ++t) {
+      int id_lane = 0;               // dQ: entry 32 (t / 32) + lane
+      for (int t = 0; t < n; ++t, ++T) {
         int j;
         if constexpr (kKeys) {
           while (left == 0) {  // warp-uniform; ends: n bits are set
@@ -207,242 +222,279 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
           if ((t & 31) == 0) id_lane = t + lane < n ? __ldg(ids + t + lane) : 0;
           j = __shfl_sync(0xffffffffu, id_lane, t & 31);
         }
-        const int s = t % stages, round = t / stages;
-        if (round > 0 && !warp_wait(bar(free0 + s), (round - 1) & 1, ctl)) break;
+        const uint32_t s = T % stages, round = T / stages;
+        if (round > 0 && !warp_wait(bar(free0 + s), (round - 1) & 1, ctl)) { ok = false; break; }
         if (lane == 0) {
-          const uint32_t full = bar(full0 + s);
+          const uint32_t b = bar(full0 + s);
           const bool stats = kKeys && first;
-          mbar_arrive_tx(full, kTile + (stats ? 2 * kStatBytes : 0));
+          mbar_arrive_tx(b, kTile + (stats ? 2 * kStatBytes : 0));
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_2d(ring + s * kTile + h * kHalf, map, 64 * h, row0 + j * kBlock, full);
+            tma_load_2d(ring + s * kTile + h * kHalf, map, 64 * h, row0 + j * kBlock, b);
           if (stats) {
             const uint32_t dst = base + kOffStats + s * 2 * kStatBytes;
             const int64_t at = (int64_t)row0 + j * kBlock;
-            bulk_load(dst, nlse + at, kStatBytes, full);
-            bulk_load(dst + kStatBytes, ndel + at, kStatBytes, full);
+            bulk_load(dst, args.nlse + at, kStatBytes, b);
+            bulk_load(dst + kStatBytes, args.ndel + at, kStatBytes, b);
           }
         }
-        issued = t + 1;
+        issued = T + 1;
       }
-      // on every path this warp's copies have landed before it leaves
-      if (lane == 0) {
-        if (first) drain_phase(bar(BA), 0);
-        for (int t = issued > stages ? issued - stages : 0; t < issued; ++t)
-          drain_phase(bar(full0 + t % stages), (t / stages) & 1);
+    }
+    // on every path this warp's copies have landed before it leaves
+    if (lane == 0) {
+      for (uint32_t x = issued > (uint32_t)stages ? issued - stages : 0; x < issued; ++x)
+        drain_phase(bar(full0 + x % stages), (x / stages) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ----------------------------------------------------------- MMA ----
+    constexpr uint32_t id_x = idesc_bf16(kBlock, kBlock, false);
+    constexpr uint32_t id_g = idesc_bf16(kBlock, D, true);
+    const uint64_t da1 = sw128_desc(base + kOffA1, 16, 1024);
+    const uint64_t da2 = sw128_desc(base + kOffA2, 16, 1024);
+    const uint64_t db1 = sw128_desc(base + kOffB1, 16, 1024);
+    const uint64_t db2 = sw128_desc(base + kOffB2, 16, 1024);
+    const uint64_t dm1 = sw128_desc(base + kOffB1, kHalf, 1024);  // MN-major
+    const uint64_t dm2 = sw128_desc(base + kOffB2, kHalf, 1024);
+    auto product = [&](uint32_t d, uint64_t a, uint64_t b) {  // d = A B^T over d
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+        mma_f16_ss(d, a + off, b + off, id_x, kk > 0 ? 1u : 0u);
       }
-    } else if (warp == kMmaWarp && lane == 0 && n > 0) {
-      // -------------------------------------------------------- MMA ----
-      constexpr uint32_t id_x = idesc_bf16(kBlock, kBlock, false);
-      constexpr uint32_t id_g = idesc_bf16(kBlock, D, true);
-      const uint64_t da1 = sw128_desc(base + kOffA1, 16, 1024);
-      const uint64_t da2 = sw128_desc(base + kOffA2, 16, 1024);
-      const uint64_t db1 = sw128_desc(base + kOffB1, 16, 1024);
-      const uint64_t db2 = sw128_desc(base + kOffB2, 16, 1024);
-      const uint64_t dm1 = sw128_desc(base + kOffB1, kHalf, 1024);  // MN-major
-      const uint64_t dm2 = sw128_desc(base + kOffB2, kHalf, 1024);
-      auto product = [&](uint32_t d, uint64_t a, uint64_t b) {  // d = A B^T over d
+    };
+    // d += A B over the tile's 128 columns, A from the elementwise threads'
+    // pairs: columns 0-31 and 64-95 of the buffer at a
+    auto gather = [&](uint32_t d, uint32_t a, uint64_t b, bool acc) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-          mma_f16_ss(d, a + off, b + off, id_x, kk > 0 ? 1u : 0u);
-        }
-      };
-      // d += A B over the tile's 128 columns, A from the elementwise
-      // threads' pairs: columns 0-31 and 64-95 of the buffer at a
-      auto gather = [&](uint32_t d, uint32_t a, uint64_t b, bool acc) {
-#pragma unroll
-        for (int kk = 0; kk < kBlock / 16; ++kk)
-          mma_f16_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + (uint64_t)(kk * 128), id_g,
-                     (acc || kk > 0) ? 1u : 0u);
-      };
-      auto b1_off = [&](int t) { return (uint64_t)((t % kS1) * (kTile >> 4)); };
-      auto b2_off = [&](int t) { return (uint64_t)((t % kB2Stages) * (kTile >> 4)); };
-      auto issue_x = [&](int t) {
-        product(tmem + kColX + (kKeys ? 0 : (t & 1) * 128), da1, db1 + b1_off(t));
-        mma_commit(bar(BX + (t & 1)));
-      };
-      auto issue_y = [&](int t) {
-        product(tmem + kColY, da2, db2 + b2_off(t));
-        mma_commit(bar(BY + (t & 1)));
-      };
-      auto wait_b1 = [&](int t) { return wait_phase(bar(BB1 + t % kS1), (t / kS1) & 1, ctl); };
-      auto wait_b2 = [&](int t) {
-        return wait_phase(bar(BB2 + t % kB2Stages), (t / kB2Stages) & 1, ctl);
-      };
-      bool ok = wait_phase(bar(BA), 0, ctl) && wait_b1(0);
-      if (ok) issue_x(0);
-      ok = ok && wait_b2(0);
-      if (ok) issue_y(0);
+      for (int kk = 0; kk < kBlock / 16; ++kk)
+        mma_f16_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + (uint64_t)(kk * 128), id_g,
+                   (acc || kk > 0) ? 1u : 0u);
+    };
+    auto b1_off = [&](uint32_t x) { return (uint64_t)((x % kS1) * (kTile >> 4)); };
+    auto b2_off = [&](uint32_t x) { return (uint64_t)((x % kB2Stages) * (kTile >> 4)); };
+    auto issue_x = [&](uint32_t x) {
+      product(tmem + kColX + (kKeys ? 0 : (x & 1) * 128), da1, db1 + b1_off(x));
+      mma_commit(bar(BX + (x & 1)));
+    };
+    auto issue_y = [&](uint32_t x) {
+      product(tmem + kColY, da2, db2 + b2_off(x));
+      mma_commit(bar(BY + (x & 1)));
+    };
+    auto wait_b1 = [&](uint32_t x) { return wait_phase(bar(BB1 + x % kS1), (x / kS1) & 1, ctl); };
+    auto wait_b2 = [&](uint32_t x) {
+      return wait_phase(bar(BB2 + x % kB2Stages), (x / kB2Stages) & 1, ctl);
+    };
+    // the products of one block; false when a wait ran out
+    auto block = [&]() -> bool {
+      if (!wait_phase(bar(BA), full & 1, ctl) || !wait_b1(T)) return false;
+      tc_fence_after();
+      issue_x(T);
+      if (!wait_b2(T)) return false;
+      issue_y(T);
+      if (n == 1) mma_commit(bar(BAFREE));
       if (!kKeys && n > 1) {
-        ok = ok && wait_b1(1);
-        if (ok) issue_x(1);
+        if (!wait_b1(T + 1)) return false;
+        issue_x(T + 1);
       }
-      for (int t = 0; ok && t < n; ++t) {
+      for (int t = 0; t < n; ++t) {
+        const uint32_t x = T + t;
         if constexpr (kKeys) {
-          if (!wait_phase(bar(BP), t & 1, ctl)) break;
+          if (!wait_phase(bar(BP), x & 1, ctl)) return false;
+          // the last block's sums are out of tensor memory
+          if (t == 0 && full > 0 && !wait_phase(bar(BFREE), (full - 1) & 1, ctl)) return false;
           tc_fence_after();
-          gather(tmem + kColG2, tmem + kColX, dm2 + b2_off(t), t > 0);
-          mma_commit(bar(BG2 + t % kB2Stages));
+          gather(tmem + kColG2, tmem + kColX, dm2 + b2_off(x), t > 0);
+          mma_commit(bar(BG2 + x % kB2Stages));
           if (t + 1 < n) {
-            if (!wait_b1(t + 1)) break;
-            issue_x(t + 1);
+            if (!wait_b1(x + 1)) return false;
+            issue_x(x + 1);
           }
         }
-        if (!wait_phase(bar(BS), t & 1, ctl)) break;
+        if (!wait_phase(bar(BS), x & 1, ctl)) return false;
+        if (!kKeys && t == 0 && full > 0 && !wait_phase(bar(BFREE), (full - 1) & 1, ctl))
+          return false;
         tc_fence_after();
-        gather(tmem + kColG1, tmem + kColY, dm1 + b1_off(t), t > 0);
-        mma_commit(bar(BG1 + t % kS1));
+        gather(tmem + kColG1, tmem + kColY, dm1 + b1_off(x), t > 0);
+        mma_commit(bar(BG1 + x % kS1));
         if (t + 1 < n) {
-          if (!wait_b2(t + 1)) break;
-          issue_y(t + 1);
+          if (!wait_b2(x + 1)) return false;
+          issue_y(x + 1);
+          if (t + 2 == n) mma_commit(bar(BAFREE));
         }
         if (!kKeys && t + 2 < n) {
-          if (!wait_b1(t + 2)) break;
-          issue_x(t + 2);
+          if (!wait_b1(x + 2)) return false;
+          issue_x(x + 2);
         }
       }
+      return true;
+    };
+    for (int ok = 1; ok != 0;) {
+      if (take(n) < 0) break;
+      if (n <= 0) continue;
+      if (lane == 0) ok = block() ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      T += n;
+      ++full;
+    }
+    if (lane == 0) {
       // every MMA issued above has completed once this commit fires
       mma_commit(bar(BDRAIN));
       drain_phase(bar(BDRAIN), 0);
     }
     __syncwarp();
   } else {
-    // -------------------------------------------------- elementwise ----
+    // --------------------------------------------------- elementwise ----
     const int half = warp >> 2;  // columns 64 half .. +63 of a tile
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
-    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t lane_addr = lanes + half * 64;
     const float2 sc2 = make_float2(scale_log2, scale_log2);
-    float2 nl2 = make_float2(0.f, 0.f), nd2 = nl2;  // dQ: this row's -lse, -D
-    int tail = kBlock;                              // dQ: valid keys of the last listed tile
-    if constexpr (!kKeys) {
-      const int64_t at = (int64_t)row0 + blk * kBlock + r;
-      nl2.x = nl2.y = __ldg(nlse + at);
-      nd2.x = nd2.y = __ldg(ndel + at);
-      // the list ascends: only its last entry can be the head's last block
-      if (n > 0 && __ldg(ids + n - 1) == g.NB - 1) tail = g.N - (g.NB - 1) * kBlock;
-    }
-    bool ok = true;
-    for (int t = 0; t < n; ++t) {
-      const float4* stat =
-          reinterpret_cast<const float4*>(smem_raw + kOffStats + (t & 1) * 2 * kStatBytes) +
-          half * 16;
-      if constexpr (kKeys)  // the statistics came with B1(t)
-        if (!all_wait(bar(BB1 + t % kS1), (t / kS1) & 1, ctl)) { ok = false; break; }
-      if (!warp_wait(bar(BX + (t & 1)), (t >> 1) & 1, ctl)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t x[64], pk[32];
-      tmem_ld64(lane_addr + kColX + (kKeys ? 0 : (t & 1) * 128), x);
-      float2 p[32];
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        float2 n0 = nl2, n1 = nl2;
-        if constexpr (kKeys) {
-          const float4 v = stat[c / 2];
-          n0 = make_float2(v.x, v.y);
-          n1 = make_float2(v.z, v.w);
-        }
-        const float2 e0 = ffma2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])),
-                                sc2, n0);
-        const float2 e1 = ffma2(
-            make_float2(__uint_as_float(x[2 * c + 2]), __uint_as_float(x[2 * c + 3])), sc2, n1);
-        p[c] = make_float2(ex2(e0.x), ex2(e0.y));
-        p[c + 1] = make_float2(ex2(e1.x), ex2(e1.y));
+    // the next block and, dQ, this thread's -lse and -D of it
+    int row, next_n = 0;
+    float next_nl = 0.f, next_nd = 0.f;
+    auto ahead = [&]() {
+      row = take(next_n);
+      if (!kKeys && row >= 0 && next_n > 0) {
+        const int bh = row / g.NB;
+        const int64_t at = (int64_t)bh * g.Np + (row - bh * g.NB) * kBlock + r;
+        next_nl = __ldg(args.nlse + at);
+        next_nd = __ldg(args.ndel + at);
       }
-      if constexpr (kKeys) {
+    };
+    ahead();
+    for (bool ok = true; ok && row >= 0;) {
+      n = next_n;
+      const int this_row = row, bh = row / g.NB, blk = row - bh * g.NB;
+      const float2 nl2 = make_float2(next_nl, next_nl), nd2 = make_float2(next_nd, next_nd);
+      if (n < 0) {  // a malformed list: nothing is written
+        ahead();
+        continue;
+      }
+      int tail = kBlock;  // dQ: valid keys of the last listed tile
+      // the list ascends: only its last entry can be the head's last block
+      if (!kKeys && n > 0 &&
+          __ldg(args.idx + (int64_t)this_row * args.k_max + n - 1) == g.NB - 1)
+        tail = g.N - (g.NB - 1) * kBlock;
+      for (int t = 0; t < n; ++t, ++T) {
+        const float4* stat =
+            reinterpret_cast<const float4*>(smem + kOffStats + (T & 1) * 2 * kStatBytes) + half * 16;
+        if constexpr (kKeys)  // the statistics came with B1(T)
+          if (!all_wait(bar(BB1 + T % kS1), (T / kS1) & 1, ctl)) { ok = false; break; }
+        if (!warp_wait(bar(BX + (T & 1)), (T >> 1) & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t x[64], pk[32];
+        tmem_ld64(lane_addr + kColX + (kKeys ? 0 : (T & 1) * 128), x);
+        float2 p[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(p[c].x, p[c].y);
-        tmem_st32_async(lane_addr + kColX, pk);
+        for (int c = 0; c < 32; c += 2) {
+          float2 n0 = nl2, n1 = nl2;
+          if constexpr (kKeys) {
+            const float4 v = stat[c / 2];
+            n0 = make_float2(v.x, v.y);
+            n1 = make_float2(v.z, v.w);
+          }
+          const float2 e0 = ffma2(
+              make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, n0);
+          const float2 e1 = ffma2(
+              make_float2(__uint_as_float(x[2 * c + 2]), __uint_as_float(x[2 * c + 3])), sc2, n1);
+          p[c] = make_float2(ex2(e0.x), ex2(e0.y));
+          p[c + 1] = make_float2(ex2(e1.x), ex2(e1.y));
+        }
+        if constexpr (kKeys) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(p[c].x, p[c].y);
+          tmem_st32_async(lane_addr + kColX, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(BP));
+        } else if (tail < kBlock && t == n - 1) {  // warp-uniform: pad keys
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (half * 64 + 2 * c >= tail) p[c].x = 0.f;
+            if (half * 64 + 2 * c + 1 >= tail) p[c].y = 0.f;
+          }
+        }
+        if (!warp_wait(bar(BY + (T & 1)), (T >> 1) & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        tmem_ld64(lane_addr + kColY, x);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float2 n0 = nd2, n1 = nd2;
+          if constexpr (kKeys) {
+            const float4 v = stat[kBlock / 4 + c / 2];
+            n0 = make_float2(v.x, v.y);
+            n1 = make_float2(v.z, v.w);
+          }
+          const float2 s0 = fmul2(
+              p[c],
+              fadd2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), n0));
+          const float2 s1 = fmul2(
+              p[c + 1],
+              fadd2(make_float2(__uint_as_float(x[2 * c + 2]), __uint_as_float(x[2 * c + 3])), n1));
+          pk[c] = pack_bf16(s0.x, s0.y);
+          pk[c + 1] = pack_bf16(s1.x, s1.y);
+        }
+        tmem_st32_async(lane_addr + kColY, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(BP));
-      } else if (tail < kBlock && t == n - 1) {  // warp-uniform: pad keys
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          if (half * 64 + 2 * c >= tail) p[c].x = 0.f;
-          if (half * 64 + 2 * c + 1 >= tail) p[c].y = 0.f;
-        }
+        mbar_arrive(bar(BS));
       }
-      if (!warp_wait(bar(BY + (t & 1)), (t >> 1) & 1, ctl)) { ok = false; break; }
-      tc_fence_after();
-      tmem_ld64(lane_addr + kColY, x);
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        float2 n0 = nd2, n1 = nd2;
-        if constexpr (kKeys) {
-          const float4 v = stat[kBlock / 4 + c / 2];
-          n0 = make_float2(v.x, v.y);
-          n1 = make_float2(v.z, v.w);
-        }
-        const float2 s0 = fmul2(
-            p[c], fadd2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), n0));
-        const float2 s1 = fmul2(
-            p[c + 1],
-            fadd2(make_float2(__uint_as_float(x[2 * c + 2]), __uint_as_float(x[2 * c + 3])), n1));
-        pk[c] = pack_bf16(s0.x, s0.y);
-        pk[c + 1] = pack_bf16(s1.x, s1.y);
-      }
-      tmem_st32_async(lane_addr + kColY, pk);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(BS));
-    }
-    // ---- epilogue: column half `half` of the row's sums, to the natural
-    // position of its token
-    if (run && ok) {
-      const int p = blk * kBlock + r;
+      if (!ok) break;
+      ahead();
+      // ---- the block's sums: column half `half` of this thread's row, as
+      // bf16 pairs in registers, then to the natural position of its token
+      constexpr int kPairs = D / 4;
+      const int pos = blk * kBlock + r;
       const int64_t at =
-          p < g.N ? (bh * g.N + natural_index(g, order, p)) * D + half * (D / 2) : -1;
-      if (n > 0) {
-        const int last = n - 1;
-        ok = warp_wait(bar(BG1 + last % kS1), (last / kS1) & 1, ctl);
-        if (kKeys && ok) ok = warp_wait(bar(BG2 + last % kB2Stages), (last / kB2Stages) & 1, ctl);
-        tc_fence_after();
-      }
-      auto store = [&](uint32_t col, float mul, __nv_bfloat16* dst) {
-#pragma unroll 1
+          pos < g.N ? ((int64_t)bh * g.N + natural_index(g, g.perm[bh % g.heads], pos)) * D +
+                          half * (D / 2)
+                    : -1;
+      uint32_t o1[kPairs], o2[kKeys ? kPairs : 1];
+      auto sums = [&](uint32_t col, float mul, uint32_t (&o)[kPairs]) {
+#pragma unroll
         for (int c0 = 0; c0 < D / 2; c0 += 32) {
-          uint32_t o[32];
-          if (n > 0) {
-            // lane_addr already holds 64 * half: d = 64's halves are 32 wide
-            tmem_ld32(lane_addr + col - half * (64 - D / 2) + c0, o);
-          } else {
+          uint32_t f[32];
+          tmem_ld32(lanes + col + half * (D / 2) + c0, f);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = 0u;
-          }
-          if (at >= 0) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint4 w;
-              w.x = pack_bf16(__uint_as_float(o[8 * c + 0]) * mul, __uint_as_float(o[8 * c + 1]) * mul);
-              w.y = pack_bf16(__uint_as_float(o[8 * c + 2]) * mul, __uint_as_float(o[8 * c + 3]) * mul);
-              w.z = pack_bf16(__uint_as_float(o[8 * c + 4]) * mul, __uint_as_float(o[8 * c + 5]) * mul);
-              w.w = pack_bf16(__uint_as_float(o[8 * c + 6]) * mul, __uint_as_float(o[8 * c + 7]) * mul);
-              reinterpret_cast<uint4*>(dst + at + c0)[c] = w;
-            }
-          }
+          for (int c = 0; c < 16; ++c)
+            o[c0 / 2 + c] =
+                pack_bf16(__uint_as_float(f[2 * c]) * mul, __uint_as_float(f[2 * c + 1]) * mul);
         }
       };
-      if (ok) {
-        store(kColG1, scale, g1);
-        if constexpr (kKeys) store(kColG2, 1.f, g2);
+      if (n > 0) {
+        const uint32_t last = T - 1;
+        ok = warp_wait(bar(BG1 + last % kS1), (last / kS1) & 1, ctl);
+        if (kKeys && ok) ok = warp_wait(bar(BG2 + last % kB2Stages), (last / kB2Stages) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        sums(kColG1, scale, o1);
+        if constexpr (kKeys) sums(kColG2, 1.f, o2);
+        tc_fence_before();
+        mbar_arrive(bar(BFREE));
+      } else {
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          o1[c] = 0u;
+          if constexpr (kKeys) o2[c] = 0u;
+        }
+      }
+      if (at >= 0) {
+#pragma unroll
+        for (int c = 0; c < kPairs / 4; ++c) {
+          reinterpret_cast<uint4*>((kKeys ? args.dk : args.dq) + at)[c] =
+              make_uint4(o1[4 * c], o1[4 * c + 1], o1[4 * c + 2], o1[4 * c + 3]);
+          if constexpr (kKeys)
+            reinterpret_cast<uint4*>(args.dv + at)[c] =
+                make_uint4(o2[4 * c], o2[4 * c + 1], o2[4 * c + 2], o2[4 * c + 3]);
+        }
       }
     }
     __syncwarp();
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kMmaWarp) {
-    __syncwarp();
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-// z = 0: the key blocks' CTAs, z = 1 the query blocks', which fill the SMs as
-// the first run out.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_sm100_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -451,10 +503,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap map_do,
                      const __grid_constant__ BwdArgs args, const __grid_constant__ Grid g,
                      float scale, float scale_log2) {
-  if (blockIdx.z == 0)
-    bwd_block<true, D>(map_k, map_v, map_q, map_do, args, g, scale, scale_log2);
-  else
-    bwd_block<false, D>(map_q, map_do, map_k, map_v, args, g, scale, scale_log2);
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t base = smem_u32(smem_raw);
+  int32_t* status = args.status;
+  if ((base & 1023u) != 0) {
+    if (threadIdx.x == 0) report(status, PA_ERR_UNSUPPORTED);
+    return;
+  }
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + kOffSlot);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const int warp = threadIdx.x >> 5;
+  const Ctl ctl{abort_flag, status, kTimeoutNs};
+  // a wait of an earlier launch already expired: end quickly
+  const bool expired =
+      status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT;
+  if (threadIdx.x == 0) {
+    for (uint32_t set = 0; set < 2; ++set)
+      for (uint32_t b = 0; b < NBAR; ++b)
+        mbar_init(base + kOffBar + (set * NBAR + b) * 8u,
+                  b == BP || b == BS || b == BFREE           ? kAluThreads
+                  : b == BTAKEN || b == BTAKEN + 1u ? kTakers
+                                                             : 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (!expired) {
+    bwd_blocks<true, D>(map_k, map_v, map_q, map_do, args, g, scale, scale_log2, smem_raw, base,
+                        tmem, ctl);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag == 0)
+      bwd_blocks<false, D>(map_q, map_do, map_k, map_v, args, g, scale, scale_log2, smem_raw, base,
+                           tmem, ctl);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 template <int D>
@@ -471,7 +565,8 @@ cudaError_t launch_typed(const BwdArgs& a, const Grid& g, cudaStream_t s) {
       !encode_tile_map(&mv, a.v, rows, D, 2, 64, kBlock) ||
       !encode_tile_map(&md, a.dop, rows, D, 2, 64, kBlock))
     return cudaErrorInvalidValue;
-  bwd_sm100_kernel<D><<<dim3(g.NB, g.B * g.heads, 2), kThreads, kSmem, s>>>(
+  const int64_t blocks = (int64_t)g.B * g.heads * g.NB;
+  bwd_sm100_kernel<D><<<(unsigned)(blocks < kSms ? blocks : kSms), kThreads, kSmem, s>>>(
       mq, mk, mv, md, a, g, (float)(1.0 / sqrt((double)D)),
       (float)(1.4426950408889634 / sqrt((double)D)));
   return cudaGetLastError();

@@ -33,6 +33,8 @@ struct BwdArgs {
   float *nlse, *ndel;              // workspace: -lse log2 e and -D of each permuted row
   uint32_t* mask;                  // workspace: [B*heads, NB, words], bit i of row j: i keeps j
   int words;
+  int32_t* checked;                // workspace: entries of each kept list, -1 if malformed
+  int32_t* counters;               // workspace: two, zero: blocks handed out
   const int32_t *idx, *counts;
   int k_max;
   __nv_bfloat16 *dq, *dk, *dv;  // natural order

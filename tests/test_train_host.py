@@ -104,8 +104,9 @@ def test_training_refusals(lib):
     assert fwd(shape=paro.PaShape(1, 2, 4, 8, 8, 64, 32)) == UNS
     assert fwd(shape=paro.PaShape(1, 2, 1, 1, 65536 * 64, 64, 64)) == UNS
     n = lib.pa_block_sparse_attn_backward_workspace(SHAPE)
-    # dO permuted, two statistics a row, one bit a pair of blocks
-    assert n == 2 * 256 * 64 * 2 + 2 * (2 * 256 * 4) + 256
+    # dO permuted, two statistics a row, one bit a pair of blocks, the lists'
+    # lengths, two counters
+    assert n == 2 * 256 * 64 * 2 + 2 * (2 * 256 * 4) + 3 * 256
     assert lib.pa_block_sparse_attn_backward_workspace(paro.PaShape(1, 2, 4, 8, 8, 65, 64)) == -1
     assert lib.pa_block_sparse_attn_backward_workspace(paro.PaShape(70000, 1, 4, 8, 8, 64, 64)) == -1
 
