@@ -20,7 +20,8 @@
 // blocks, from a counter each: a block's loads start while the last one's
 // sums are stored, and its first products follow the last one's without a
 // pause.  (A CTA per block, which starts and ends 7 us around its tiles,
-// took 299 us for the two clips of 12 tiles a block, this form 250 us.)
+// took 282 us for 740 blocks of 12 tiles, this form 269 us; 5.19 and 4.84 ms
+// for 196608 tiles in each use at d = 128.)
 //
 // 12 warps:
 //   0-7    elementwise; warp w holds lanes 32 (w % 4) .. +31 (a row a
@@ -33,19 +34,30 @@
 //   11     takes the blocks and hands them to the other warps, two ahead.
 // The tiles of a CTA's blocks are numbered through (T below): stages and
 // barrier phases go on from block to block.
-// Tensor memory, 512 columns: kKeys X 0, Y 128, G1 256, G2 384; dQ X0 0,
-// X1 128, Y 256, G1 384.  A thread writes its P (or dS) as bf16 pairs over
-// the columns of X (or Y) that it read itself: 32 columns from column 64 g
-// of the buffer, g the column half.
-// Issue order, kKeys: X0 Y0, then for every t: G2(t) X(t+1) G1(t) Y(t+1):
-// P(t+1) has the time of G1(t) and Y(t+1), dS(t) that of G2(t) and X(t+1).
-// dQ: X0 Y0 X1, then G1(t) Y(t+1) X(t+2).  X(t+1) overwrites the P(t) that
-// G2(t) reads, and Y(t+1) the dS(t) of G1(t): MMAs that one thread issues
-// run in order in the tensor pipe.
+// Tensor memory, 512 columns: kKeys at d = 128: X 0, Y 128, G1 256, G2 384;
+// otherwise X0 0, X1 128, Y 256, G1 384 (and kKeys, d = 64, G2 448).  A thread
+// writes its P (or dS) as bf16 pairs over the columns of X (or Y) that it
+// read itself: 32 columns from column 64 g of the buffer, g the column half.
+// Issue order with one X (kKeys, d = 128): X0 Y0, then for every t: G2(t)
+// X(t+1) G1(t) Y(t+1): P(t+1) has the time of G1(t) and Y(t+1), dS(t) that of
+// G2(t) and X(t+1).  With two: X0 Y0 X1, then (kKeys G2(t)) G1(t) Y(t+1)
+// X(t+2).  An X overwrites a P that an earlier G2 reads, and Y(t+1) the
+// dS(t) of G1(t): MMAs that one thread issues run in order in the tensor
+// pipe.
 //
-// Bounded by the MMA stream (4 products a tile with kKeys, 3 for dQ); the
-// exponentials take 16384 / 16 = 1024 cycles a tile of the 3000.  Waits are
-// bounded as in the forward kernel.
+// P and dS are rounded to bf16 (2^-8 of their value at most) for the second
+// products, as P is in the forward kernel; the sums stay in 32 bits.  The
+// rounding of dS is what dq and dk carry most of: 0.0025 relative in the
+// norm, against 0.0017 of rounding the result alone.  (dS as two bf16 halves
+// would bring it to the latter, for one more product a tile in each use.)
+//
+// Bounded by the MMA stream (4 products a tile with kKeys, 3 for dQ) at
+// d = 128: 3040 of the 3480 cycles that a kKeys tile takes, 1.2 PFLOP/s over
+// both uses, at the clock that the power limit leaves.  At d = 64 the chain
+// X, P, dS, G of one tile bounds it: 85 us for 2556 tiles with two X's, 91 us
+// with one.  The exponentials take 16384 / 16 = 1024 cycles a tile.
+// 16 elementwise warps instead of 8 changed nothing (4.92 and 4.84 ms).
+// Waits are bounded as in the forward kernel.
 #include "bwd.cuh"
 #include "sm100.cuh"
 
@@ -65,9 +77,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOffBar = 0;      // two sets of NBAR barriers: kKeys, dQ
 constexpr uint32_t kOffSlot = 512;   // tensor memory's base, the abort flag
 constexpr uint32_t kOffItems = 528;  // [2 sets][2] of (block of the grid, tiles)
-constexpr uint32_t kOffStats = 1024;  // kKeys: [2 stages][-lse, -D][128] float
+constexpr uint32_t kOffStats = 1024;  // kKeys: [B1 stage][-lse, -D][128] float
 constexpr uint32_t kStatBytes = kBlock * 4;
-constexpr uint32_t kSmall = 3072;  // operand tiles from here, 1024-aligned
 
 enum : uint32_t {
   BA = 0,      // A1, A2 of the block loaded
@@ -87,11 +98,19 @@ enum : uint32_t {
   NBAR = 24
 };
 static_assert(2 * NBAR * 8 <= kOffSlot, "barrier region");
-static_assert(kOffStats + 4 * kStatBytes <= kSmall, "statistics region");
 constexpr uint32_t kTakers = 8 + 2 + 1;  // elementwise warps, loaders, MMA
 
-template <bool kKeys>
-constexpr int kB1Stages = kKeys ? 2 : 3;
+// X in two buffers, so that X(T + 1) is there when the elementwise threads
+// come to it: for dQ, and for dK, dV at d = 64, where tensor memory has the
+// room.  X(T + 2) is then issued with G1(T), and B1 takes three stages.
+template <bool kKeys, int D>
+constexpr bool kTwoX = !kKeys || D == 64;
+template <bool kKeys, int D>
+constexpr int kB1Stages = kTwoX<kKeys, D> ? 3 : 2;
+// operand tiles from here, 1024-aligned
+template <int D>
+constexpr uint32_t kSmall =
+    (kOffStats + kB1Stages<true, D> * 2 * kStatBytes + 1023) / 1024 * 1024;
 constexpr int kB2Stages = 2;
 
 // Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
@@ -113,11 +132,12 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
                                            float scale_log2, unsigned char* smem, uint32_t base,
                                            uint32_t tmem, Ctl ctl) {
   constexpr uint32_t kTile = kBlock * D * 2;
-  constexpr int kS1 = kB1Stages<kKeys>;
-  constexpr uint32_t kOffA1 = kSmall, kOffA2 = kOffA1 + kTile, kOffB1 = kOffA2 + kTile,
+  constexpr int kS1 = kB1Stages<kKeys, D>;
+  constexpr bool kTwo = kTwoX<kKeys, D>;
+  constexpr uint32_t kOffA1 = kSmall<D>, kOffA2 = kOffA1 + kTile, kOffB1 = kOffA2 + kTile,
                      kOffB2 = kOffB1 + kS1 * kTile;
-  constexpr uint32_t kColX = 0, kColY = kKeys ? 128 : 256, kColG1 = kKeys ? 256 : 384,
-                     kColG2 = 384;
+  constexpr uint32_t kColX = 0, kColY = kTwo ? 256 : 128, kColG1 = kTwo ? 384 : 256,
+                     kColG2 = kColG1 + D;
   auto bar = [&](uint32_t slot) {
     return base + kOffBar + ((kKeys ? 0u : (uint32_t)NBAR) + slot) * 8u;
   };
@@ -274,7 +294,7 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
     auto b1_off = [&](uint32_t x) { return (uint64_t)((x % kS1) * (kTile >> 4)); };
     auto b2_off = [&](uint32_t x) { return (uint64_t)((x % kB2Stages) * (kTile >> 4)); };
     auto issue_x = [&](uint32_t x) {
-      product(tmem + kColX + (kKeys ? 0 : (x & 1) * 128), da1, db1 + b1_off(x));
+      product(tmem + kColX + (kTwo ? (x & 1) * 128 : 0), da1, db1 + b1_off(x));
       mma_commit(bar(BX + (x & 1)));
     };
     auto issue_y = [&](uint32_t x) {
@@ -293,7 +313,7 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
       if (!wait_b2(T)) return false;
       issue_y(T);
       if (n == 1) mma_commit(bar(BAFREE));
-      if (!kKeys && n > 1) {
+      if (kTwo && n > 1) {
         if (!wait_b1(T + 1)) return false;
         issue_x(T + 1);
       }
@@ -304,9 +324,9 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
           // the last block's sums are out of tensor memory
           if (t == 0 && full > 0 && !wait_phase(bar(BFREE), (full - 1) & 1, ctl)) return false;
           tc_fence_after();
-          gather(tmem + kColG2, tmem + kColX, dm2 + b2_off(x), t > 0);
+          gather(tmem + kColG2, tmem + kColX + (kTwo ? (x & 1) * 128 : 0), dm2 + b2_off(x), t > 0);
           mma_commit(bar(BG2 + x % kB2Stages));
-          if (t + 1 < n) {
+          if (!kTwo && t + 1 < n) {
             if (!wait_b1(x + 1)) return false;
             issue_x(x + 1);
           }
@@ -322,7 +342,7 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
           issue_y(x + 1);
           if (t + 2 == n) mma_commit(bar(BAFREE));
         }
-        if (!kKeys && t + 2 < n) {
+        if (kTwo && t + 2 < n) {
           if (!wait_b1(x + 2)) return false;
           issue_x(x + 2);
         }
@@ -379,13 +399,14 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
         tail = g.N - (g.NB - 1) * kBlock;
       for (int t = 0; t < n; ++t, ++T) {
         const float4* stat =
-            reinterpret_cast<const float4*>(smem + kOffStats + (T & 1) * 2 * kStatBytes) + half * 16;
+            reinterpret_cast<const float4*>(smem + kOffStats + (T % kS1) * 2 * kStatBytes) + half * 16;
         if constexpr (kKeys)  // the statistics came with B1(T)
           if (!all_wait(bar(BB1 + T % kS1), (T / kS1) & 1, ctl)) { ok = false; break; }
         if (!warp_wait(bar(BX + (T & 1)), (T >> 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         uint32_t x[64], pk[32];
-        tmem_ld64(lane_addr + kColX + (kKeys ? 0 : (T & 1) * 128), x);
+        const uint32_t x_col = lane_addr + kColX + (kTwo ? (T & 1) * 128 : 0);
+        tmem_ld64(x_col, x);
         float2 p[32];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
@@ -405,7 +426,7 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
         if constexpr (kKeys) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(p[c].x, p[c].y);
-          tmem_st32_async(lane_addr + kColX, pk);
+          tmem_st32_async(x_col, pk);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(bar(BP));
@@ -554,8 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch_typed(const BwdArgs& a, const Grid& g, cudaStream_t s) {
   constexpr uint32_t kTile = kBlock * D * 2;
-  constexpr int kSmem = kSmall + (2 + kB1Stages<false> + kB2Stages) * kTile;
-  static_assert(kSmem <= kSmemOptIn && kB1Stages<true> <= kB1Stages<false>, "shared memory");
+  constexpr int kSmem = kSmall<D> + (2 + kB1Stages<false, D> + kB2Stages) * kTile;
+  static_assert(kSmem <= kSmemOptIn && kB1Stages<true, D> <= kB1Stages<false, D>, "shared memory");
   const cudaError_t e = opt_in_smem<bwd_sm100_kernel<D>>(kSmem);
   if (e != cudaSuccess) return e;
   const uint64_t rows = (uint64_t)g.B * g.heads * g.Np;
