@@ -4,7 +4,8 @@
 // of attn_bwd.cu.  (tcgen05 works on 128 rows at a time.)
 //
 // A CTA owns a block of 64 rows and goes over the 64-column tiles of its
-// list, the next tiles on their way (cp.async) while it works on this one.  Eight warps: warp w owns rows 16 (w % 4) .. +15 and the columns
+// list, the next tiles on their way (cp.async) while it works on this one.
+// Eight warps: warp w owns rows 16 (w % 4) .. +15 and the columns
 // 32 (w / 4) .. +31 of every tile; the two column halves keep their own sums
 // and join once at the end.  Such tiles are small (64 KFLOP a warp and
 // product at d = 64), so latency bounds a list's walk: with one tile in

@@ -5,20 +5,25 @@
 #include "common.cuh"
 
 #include <atomic>
+#include <mutex>
 
 namespace paro {
 
 // Opts kernel Kern into `bytes` of dynamic shared memory on the current
 // device (kClusters: and into clusters of more than 8 CTAs), once for each
 // size that grows: the attribute outlives the call, and setting it every
-// time is a microsecond of a small call.
+// time is a microsecond of a small call.  (Under a lock: of two threads that
+// set it at once the smaller size could stay.)
 template <auto Kern, bool kClusters = false>
 cudaError_t opt_in_smem(int bytes) {
   constexpr int kDevices = 64;
   static std::atomic<int> done[kDevices];
+  static std::mutex mutex;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < kDevices && done[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  const std::lock_guard<std::mutex> lock(mutex);
   if (dev < kDevices && done[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (kClusters && e == cudaSuccess)

@@ -597,7 +597,7 @@ def _row_shape(B, heads, F, H, W, d):
 class RopeTable:
     """Rotary positions with three axes (time, height, width): the cosines
     and sines of every coordinate of ``extent`` = (frames, height, width),
-    made once on the device and kept by the caller.
+    made once, on the device and its current stream, and kept by the caller.
 
     ``pairs``: how many of the head dimension's d/2 pairs turn with each axis,
     in that order (the rest stay); default: a third of them each to height
@@ -678,8 +678,8 @@ def rope3d(x, rope: RopeTable, positions=None, inverse=False, out=None, status=N
     as ``.transpose(1, 2)``.  Token n sits at its place in ``grid`` (frames,
     height, width; by default ``rope.extent``, which has to cover it), or at
     ``positions`` (int32 [N, 3] or [B, N, 3], contiguous; a coordinate
-    outside the table is reported on ``status`` and its rows stay unwritten).  ``inverse`` turns
-    back: the gradient's rotation.  ``out``: any non-overlapping strides, or
+    outside the table is reported on ``status`` and its rows stay unwritten).
+    ``inverse`` turns back: the gradient's rotation.  ``out``: any non-overlapping strides, or
     x itself (not a tensor that shares only part of x's memory); contiguous
     by default."""
     i = _rope_checks(x, rope, rope.d)
@@ -755,7 +755,8 @@ def block_sparse_attn_lse(q, k, v, pr: Problem, idx, counts=None, out=None, lse=
     else:
         _need(i, "lse", lse, pr.rows, torch.float32)
     _launch(q, load().pa_block_sparse_attn_lse, q.data_ptr(), k.data_ptr(), v.data_ptr(), PA_BF16,
-            pr.shape, pr.perms_ptr, _addr(idx), _addr(counts), idx.shape[3], out.data_ptr(), lse.data_ptr(), _addr(status))
+            pr.shape, pr.perms_ptr, _addr(idx), _addr(counts), idx.shape[3], out.data_ptr(),
+            lse.data_ptr(), _addr(status))
     return out, lse
 
 

@@ -489,8 +489,9 @@ PA_API pa_status pa_block_sparse_attn_lse(const void* q, const void* k, const vo
  * does not take. */
 PA_API int64_t pa_block_sparse_attn_backward_workspace(pa_shape shape);
 
-/* The backward pass, gradients of pa_block_sparse_attn_lse (PA_BF16): with P = exp(S - lse) on
- * the kept tiles, D_n = dout_n . out_n - dlse_n, dS = P o (dout V^T - D),
+/* The backward pass, gradients of pa_block_sparse_attn_lse (PA_BF16): with
+ * P = exp(S - lse) on the kept tiles, D_n = dout_n . out_n - dlse_n and
+ * dS = P o (dout V^T - D),
  *   dq = dS K / sqrt(d),  dk = dS^T Q / sqrt(d),  dv = P^T dout.
  * q, k, v: the permuted copies that the forward pass took; dout, out, dq,
  * dk, dv [B,heads,N,d] bf16 natural order; lse, dlse (may be NULL: zero)
@@ -512,7 +513,7 @@ PA_API pa_status pa_block_sparse_attn_backward(
 /* ---- Serving: single query tokens against a stored clip ---------------
  *
  * Query row m of head hq (key head hq / q_group): block scores q . k_pool_j
- * (summed in 64 bits; NaN read as -inf), the k_keep blocks with the largest
+ * (held as two floats, some 46 bits; NaN read as -inf), the k_keep blocks with the largest
  * (ties to the lower index), softmax attention over their tokens:
  *   out[b,hq,m,:] = sum_c softmax_c(q . k_c / sqrt(d)) v_c.
  * q, out [B, heads*q_group, M, d]; k, v [B,heads,N_p,d] in the permuted
