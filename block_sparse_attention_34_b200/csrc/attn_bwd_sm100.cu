@@ -349,15 +349,15 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
       }
       return true;
     };
-    for (int ok = 1; ok != 0;) {
+    for (bool ok = true; ok;) {
       if (take(n) < 0) break;
       if (n <= 0) continue;
-      if (lane == 0) ok = block() ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = !elect_one() || block();
+      ok = __all_sync(0xffffffffu, ok);
       T += n;
       ++full;
     }
-    if (lane == 0) {
+    if (elect_one()) {  // (the same lane every time)
       // every MMA issued above has completed once this commit fires
       mma_commit(bar(BDRAIN));
       drain_phase(bar(BDRAIN), 0);

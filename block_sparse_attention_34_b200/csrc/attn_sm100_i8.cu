@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA ----
-    if (lane == 0 && n_tiles > 0) {
+    if (n_tiles > 0 && elect_one()) {
       constexpr uint32_t id_qk = idesc_s8(kBlock, kBlock, false);
       constexpr uint32_t id_pv = idesc_s8(kBlock, kD, true);
       bool ok = wait_phase(bar(BQ), 0, ctl);
