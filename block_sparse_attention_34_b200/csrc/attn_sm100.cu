@@ -442,7 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // barriers of the next group are tested (without blocking) before the
       // current group is issued, so that a blocking wait is left only when
       // that test failed.
-      if (n_tiles > 0 && elect_one()) {
+      // (Not an elected lane at d = 64: its products are half as long, and
+      // issued without a pause they bring the two groups' tiles at once:
+      // 24 tiles a block took 108 us instead of 95.)
+      if (n_tiles > 0 && (kD == 64 ? lane == 0 : elect_one())) {
         constexpr uint32_t id_qk = idesc_bf16(kBlock, kBlock, false);
         constexpr uint32_t id_pv = idesc_bf16(kBlock, kD, true);
         // descriptors of stage 0 / of Q; other stages and k-steps add their
