@@ -20,8 +20,7 @@
 // blocks, from a counter each: a block's loads start while the last one's
 // sums are stored, and its first products follow the last one's without a
 // pause.  (A CTA per block, which starts and ends 7 us around its tiles,
-// took 282 us for 740 blocks of 12 tiles, this form 269 us; 5.19 and 4.84 ms
-// for 196608 tiles in each use at d = 128.)
+// took 4 to 7% longer.)
 //
 // 12 warps:
 //   0-7    elementwise; warp w holds lanes 32 (w % 4) .. +31 (a row a
@@ -35,15 +34,16 @@
 // The tiles of a CTA's blocks are numbered through (T below): stages and
 // barrier phases go on from block to block.
 // Tensor memory, 512 columns: kKeys at d = 128: X 0, Y 128, G1 256, G2 384;
-// otherwise X0 0, X1 128, Y 256, G1 384 (and kKeys, d = 64, G2 448).  A thread
-// writes its P (or dS) as bf16 pairs over the columns of X (or Y) that it
-// read itself: 32 columns from column 64 g of the buffer, g the column half.
-// Issue order with one X (kKeys, d = 128): X0 Y0, then for every t: G2(t)
-// X(t+1) G1(t) Y(t+1): P(t+1) has the time of G1(t) and Y(t+1), dS(t) that of
-// G2(t) and X(t+1).  With two: X0 Y0 X1, then (kKeys G2(t)) G1(t) Y(t+1)
-// X(t+2).  An X overwrites a P that an earlier G2 reads, and Y(t+1) the
-// dS(t) of G1(t): MMAs that one thread issues run in order in the tensor
-// pipe.
+// otherwise three buffers at 0, 128, 256 that X and Y go round, G1 384 (and
+// kKeys, d = 64, G2 448).  A thread writes its P (or dS) as bf16 pairs over
+// the columns of X (or Y) that it read itself: 32 columns from column 64 g
+// of the buffer, g the column half.
+// Issue order with one X and one Y (kKeys, d = 128): X0 Y0, then for every t:
+// G2(t) X(t+1) G1(t) Y(t+1): P(t+1) has the time of G1(t) and Y(t+1), dS(t)
+// that of G2(t) and X(t+1).  With three buffers: X0 Y0 X1, then (kKeys G2(t))
+// Y(t+1) G1(t) X(t+2).  A product overwrites a P or dS that an earlier one
+// reads, MMAs that one thread issues run in order in the tensor pipe, or an X
+// that the elementwise threads have read (dQ: they say so in place of P).
 //
 // P and dS are rounded to bf16 (2^-8 of their value at most) for the second
 // products, as P is in the forward kernel; the sums stay in 32 bits.  The
@@ -51,12 +51,14 @@
 // norm, against 0.0017 of rounding the result alone.  (dS as two bf16 halves
 // would bring it to the latter, for one more product a tile in each use.)
 //
-// Bounded by the MMA stream (4 products a tile with kKeys, 3 for dQ) at
-// d = 128: 3040 of the 3480 cycles that a kKeys tile takes, 1.2 PFLOP/s over
-// both uses, at the clock that the power limit leaves.  At d = 64 the chain
-// X, P, dS, G of one tile bounds it: 85 us for 2556 tiles with two X's, 91 us
-// with one.  The exponentials take 16384 / 16 = 1024 cycles a tile.
-// 16 elementwise warps instead of 8 changed nothing (4.92 and 4.84 ms).
+// Measured, d = 128: 196608 tiles in each use 4.18 ms, 1.38 PFLOP/s with the
+// products computed twice, at the clock that the power limit leaves (some
+// 1.7 GHz); 740 blocks of 12 tiles 234 us; d = 64, 2556 tiles 75 us.  Bounded
+// by the MMA stream and the power limit; with short lists by the gap between
+// two blocks (6000 cycles, of which the sums' way out is half; four warps of
+// their own for it gained 8 us of 240 there and lost 2% on long lists).  X in
+// two buffers and one Y: 4.24 ms, 241 us, 78 us.  16 elementwise warps changed
+// nothing.  The exponentials take 16384 / 16 = 1024 cycles a tile.
 // Waits are bounded as in the forward kernel.
 #include "bwd.cuh"
 #include "sm100.cuh"
@@ -88,25 +90,26 @@ enum : uint32_t {
   BY = 8,      // Y(T) complete (ring of 2)
   BG1 = 10,    // G1(T) complete: its B1 stage is free (3)
   BG2 = 13,    // G2(T) complete: its B2 stage is free (2)
-  BP = 15,     // P(T) written by every elementwise thread
-  BS = 16,     // dS(T) written
-  BFREE = 17,  // the block's sums read by every elementwise thread
-  BAFREE = 18,  // the block's last product that reads A1 or A2 (Y) complete
-  BDRAIN = 19,
-  BITEM = 20,   // a block handed out (ring of 2)
-  BTAKEN = 22,  // and taken by every warp (2)
-  NBAR = 24
+  BP = 15,     // P(T) written by every elementwise thread (dQ: X(T) read; ring of 2:
+  BS = 17,     // dS(T) written (2)         they may be a tile ahead of the MMA thread)
+  BFREE = 19,  // the block's sums read by every elementwise thread
+  BAFREE = 20,  // the block's last product that reads A1 or A2 (Y) complete
+  BDRAIN = 21,
+  BITEM = 22,   // a block handed out (ring of 2)
+  BTAKEN = 24,  // and taken by every warp (2)
+  NBAR = 26
 };
 static_assert(2 * NBAR * 8 <= kOffSlot, "barrier region");
 constexpr uint32_t kTakers = 8 + 2 + 1;  // elementwise warps, loaders, MMA
 
-// X in two buffers, so that X(T + 1) is there when the elementwise threads
-// come to it: for dQ, and for dK, dV at d = 64, where tensor memory has the
-// room.  X(T + 2) is then issued with G1(T), and B1 takes three stages.
+// X and Y in three buffers that go round (X(T), Y(T), X(T + 1), Y(T + 1), ...)
+// for dQ, and for dK, dV at d = 64, where tensor memory has the room: the
+// elementwise threads find the next X and the next Y done.  X(T + 2) is then
+// issued with G1(T), and B1 takes three stages.
 template <bool kKeys, int D>
-constexpr bool kTwoX = !kKeys || D == 64;
+constexpr bool kRound = !kKeys || D == 64;
 template <bool kKeys, int D>
-constexpr int kB1Stages = kTwoX<kKeys, D> ? 3 : 2;
+constexpr int kB1Stages = kRound<kKeys, D> ? 3 : 2;
 // operand tiles from here, 1024-aligned
 template <int D>
 constexpr uint32_t kSmall =
@@ -133,11 +136,12 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
                                            uint32_t tmem, Ctl ctl) {
   constexpr uint32_t kTile = kBlock * D * 2;
   constexpr int kS1 = kB1Stages<kKeys, D>;
-  constexpr bool kTwo = kTwoX<kKeys, D>;
+  constexpr bool kThree = kRound<kKeys, D>;
   constexpr uint32_t kOffA1 = kSmall<D>, kOffA2 = kOffA1 + kTile, kOffB1 = kOffA2 + kTile,
                      kOffB2 = kOffB1 + kS1 * kTile;
-  constexpr uint32_t kColX = 0, kColY = kTwo ? 256 : 128, kColG1 = kTwo ? 384 : 256,
-                     kColG2 = kColG1 + D;
+  constexpr uint32_t kColG1 = kThree ? 384 : 256, kColG2 = kColG1 + D;
+  auto col_x = [](uint32_t x) { return kThree ? 2 * x % 3 * 128 : 0; };
+  auto col_y = [](uint32_t x) { return kThree ? (2 * x + 1) % 3 * 128 : 128; };
   auto bar = [&](uint32_t slot) {
     return base + kOffBar + ((kKeys ? 0u : (uint32_t)NBAR) + slot) * 8u;
   };
@@ -294,11 +298,11 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
     auto b1_off = [&](uint32_t x) { return (uint64_t)((x % kS1) * (kTile >> 4)); };
     auto b2_off = [&](uint32_t x) { return (uint64_t)((x % kB2Stages) * (kTile >> 4)); };
     auto issue_x = [&](uint32_t x) {
-      product(tmem + kColX + (kTwo ? (x & 1) * 128 : 0), da1, db1 + b1_off(x));
+      product(tmem + col_x(x), da1, db1 + b1_off(x));
       mma_commit(bar(BX + (x & 1)));
     };
     auto issue_y = [&](uint32_t x) {
-      product(tmem + kColY, da2, db2 + b2_off(x));
+      product(tmem + col_y(x), da2, db2 + b2_off(x));
       mma_commit(bar(BY + (x & 1)));
     };
     auto wait_b1 = [&](uint32_t x) { return wait_phase(bar(BB1 + x % kS1), (x / kS1) & 1, ctl); };
@@ -313,38 +317,46 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
       if (!wait_b2(T)) return false;
       issue_y(T);
       if (n == 1) mma_commit(bar(BAFREE));
-      if (kTwo && n > 1) {
+      if (kThree && n > 1) {
         if (!wait_b1(T + 1)) return false;
         issue_x(T + 1);
       }
+      // Y(x), and whether it was the block's last product with A1 or A2
+      auto next_y = [&](uint32_t x) {
+        if (!wait_b2(x)) return false;
+        issue_y(x);
+        if (x + 1 == T + n) mma_commit(bar(BAFREE));
+        return true;
+      };
       for (int t = 0; t < n; ++t) {
         const uint32_t x = T + t;
+        if (!wait_phase(bar(BP + (x & 1)), (x >> 1) & 1, ctl)) return false;
+        // the last block's sums are out of tensor memory
+        if (t == 0 && full > 0 && !wait_phase(bar(BFREE), (full - 1) & 1, ctl)) return false;
+        tc_fence_after();
         if constexpr (kKeys) {
-          if (!wait_phase(bar(BP), x & 1, ctl)) return false;
-          // the last block's sums are out of tensor memory
-          if (t == 0 && full > 0 && !wait_phase(bar(BFREE), (full - 1) & 1, ctl)) return false;
-          tc_fence_after();
-          gather(tmem + kColG2, tmem + kColX + (kTwo ? (x & 1) * 128 : 0), dm2 + b2_off(x), t > 0);
+          gather(tmem + kColG2, tmem + col_x(x), dm2 + b2_off(x), t > 0);
           mma_commit(bar(BG2 + x % kB2Stages));
-          if (!kTwo && t + 1 < n) {
+        }
+        if (t + 1 < n) {
+          if constexpr (kThree) {
+            if (!next_y(x + 1)) return false;
+          } else {
             if (!wait_b1(x + 1)) return false;
             issue_x(x + 1);
           }
         }
-        if (!wait_phase(bar(BS), x & 1, ctl)) return false;
-        if (!kKeys && t == 0 && full > 0 && !wait_phase(bar(BFREE), (full - 1) & 1, ctl))
-          return false;
+        if (!wait_phase(bar(BS + (x & 1)), (x >> 1) & 1, ctl)) return false;
         tc_fence_after();
-        gather(tmem + kColG1, tmem + kColY, dm1 + b1_off(x), t > 0);
+        gather(tmem + kColG1, tmem + col_y(x), dm1 + b1_off(x), t > 0);
         mma_commit(bar(BG1 + x % kS1));
-        if (t + 1 < n) {
-          if (!wait_b2(x + 1)) return false;
-          issue_y(x + 1);
-          if (t + 2 == n) mma_commit(bar(BAFREE));
-        }
-        if (kTwo && t + 2 < n) {
-          if (!wait_b1(x + 2)) return false;
-          issue_x(x + 2);
+        if constexpr (kThree) {
+          if (t + 2 < n) {
+            if (!wait_b1(x + 2)) return false;
+            issue_x(x + 2);
+          }
+        } else if (t + 1 < n) {
+          if (!next_y(x + 1)) return false;
         }
       }
       return true;
@@ -405,8 +417,12 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
         if (!warp_wait(bar(BX + (T & 1)), (T >> 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         uint32_t x[64], pk[32];
-        const uint32_t x_col = lane_addr + kColX + (kTwo ? (T & 1) * 128 : 0);
+        const uint32_t x_col = lane_addr + col_x(T), y_col = lane_addr + col_y(T);
         tmem_ld64(x_col, x);
+        if constexpr (!kKeys) {  // X is read: its buffer is free
+          tc_fence_before();
+          mbar_arrive(bar(BP + (T & 1)));
+        }
         float2 p[32];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
@@ -429,7 +445,7 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
           tmem_st32_async(x_col, pk);
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(bar(BP));
+          mbar_arrive(bar(BP + (T & 1)));
         } else if (tail < kBlock && t == n - 1) {  // warp-uniform: pad keys
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
@@ -439,7 +455,7 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
         }
         if (!warp_wait(bar(BY + (T & 1)), (T >> 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld64(lane_addr + kColY, x);
+        tmem_ld64(y_col, x);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
           float2 n0 = nd2, n1 = nd2;
@@ -457,10 +473,10 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
           pk[c] = pack_bf16(s0.x, s0.y);
           pk[c + 1] = pack_bf16(s1.x, s1.y);
         }
-        tmem_st32_async(lane_addr + kColY, pk);
+        tmem_st32_async(y_col, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(BS));
+        mbar_arrive(bar(BS + (T & 1)));
       }
       if (!ok) break;
       ahead();
@@ -542,9 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t set = 0; set < 2; ++set)
       for (uint32_t b = 0; b < NBAR; ++b)
         mbar_init(base + kOffBar + (set * NBAR + b) * 8u,
-                  b == BP || b == BS || b == BFREE           ? kAluThreads
+                  b >= BP && b <= BFREE             ? kAluThreads
                   : b == BTAKEN || b == BTAKEN + 1u ? kTakers
-                                                             : 1);
+                                                    : 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
