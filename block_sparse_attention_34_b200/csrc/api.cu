@@ -737,7 +737,7 @@ pa_status pa_block_sparse_attn_backward(const void* dout, const void* q, const v
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = paro::launch_bwd_prep(out, dout, lse, dlse, a, g, s);
   if (e == cudaSuccess)
-    e = g.block == 128 ? paro::launch_bwd_sm100(a, g, s) : paro::launch_bwd_mma(a, g, s);
+    e = g.block == 128 ? paro::launch_bwd_sm100(a, g, s) : paro::launch_bwd64_sm100(a, g, s);
   return cuda_status(e, "pa_block_sparse_attn_backward launch");
 }
 

@@ -8,8 +8,8 @@
 // P needs no running maximum here: lse is known from the forward pass.
 //
 // dQ sums over a query block's kept key blocks, dK and dV over the query
-// blocks that keep a key block, so two kernels (attn_bwd_sm100.cu for block
-// 128, attn_train_mma.cu for block 64), each the owner of its sums:
+// blocks that keep a key block, so each is computed by the owner of its sums
+// (attn_bwd_sm100.cu for block 128, attn_bwd64_sm100.cu for block 64):
 // no atomics, the same bits on every run, at the price of computing S and dP
 // twice (7 products a tile instead of 5; an fp32 dQ of 64 KB a tile added
 // through L2 would cost about as much as the two products).

@@ -1,16 +1,16 @@
-// Training attention at block 64 on the warp-level tensor-core path
-// (mma.sync m16n8k16, bf16 operands, fp32 sums): the forward pass with its
-// log-sum-exp, and the two gradient kernels, whose formulas are at the head
-// of attn_bwd.cu.  (tcgen05 works on 128 rows at a time.)
+// The forward pass of training attention (with its log-sum-exp) at block 64 on
+// the warp-level tensor-core path (mma.sync m16n8k16, bf16 operands, fp32
+// sums).  (A tcgen05 tile has 128 rows, or 64 in half of the lanes, where the
+// softmax then takes as long.)
 //
 // A CTA owns a block of 64 rows and goes over the 64-column tiles of its
 // list, the next tiles on their way (cp.async) while it works on this one.
 // Eight warps: warp w owns rows 16 (w % 4) .. +15 and the columns
 // 32 (w / 4) .. +31 of every tile; the two column halves keep their own sums
-// and join once at the end.  Such tiles are small (64 KFLOP a warp and
-// product at d = 64), so latency bounds a list's walk: with one tile in
-// flight and four warps a CTA the three kernels of the 2,048-token case of
-// four heads took 33 + 56 + 19 us.
+// and join once at the end.  Long lists are bound by mma.sync (307200 tiles
+// at d = 64: 1.43 ms, 1275 cycles of an SM a tile, 1024 of them products);
+// short ones by latency: 1280 tiles of 128 lists take 12.4 us, 33 us with one
+// tile in flight and four warps a CTA.
 #include "bwd.cuh"
 #include "sm100.cuh"
 
@@ -23,7 +23,6 @@ constexpr int kThreads = 256;
 // tile's work
 template <int D>
 constexpr int kStages = D == 64 ? 4 : 3;
-constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void ldsm4(const void* p, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -133,7 +132,6 @@ __device__ __forceinline__ void join(float (&acc)[D / 8][4], float* pass, int ha
   __syncthreads();
 }
 
-// ---------------------------------------------------------------- forward --
 template <int D>
 constexpr int kFwdSmem = (1 + 2 * kStages<D>) * kTileElems<D> * 2;
 static_assert(kFwdSmem<64> - kTileElems<64> * 2 >= 128 * (64 / 2) * 4, "join");
@@ -289,210 +287,6 @@ __global__ void __launch_bounds__(kThreads)
   store_rows<D>(Qs, out, g, order, bh, t);
 }
 
-// --------------------------------------------------------------- backward --
-template <int D>
-constexpr int kBwdSmem = (2 + 2 * kStages<D>) * kTileElems<D> * 2 + kStages<D> * 2 * kBlock * 4;
-
-// kKeys: one CTA per key block, dK and dV (rows are keys: A1 = K, A2 = V;
-// streamed query blocks: B1 = Q, B2 = dO).  Otherwise one CTA per query
-// block, dQ (A1 = Q, A2 = dO; streamed key blocks: B1 = K, B2 = V).  Either
-// way X = A1 B1^T are the scores and Y = A2 B2^T is dP, rows by columns of
-// the tile, G1 += dS B1 and (kKeys) G2 += P B2.  P and dS are rounded to bf16
-// for their products.
-template <int D, bool kKeys>
-__device__ __forceinline__ void bwd_block(const BwdArgs& args, const Grid& g, float scale) {
-  const __nv_bfloat16* __restrict__ a1 = kKeys ? args.k : args.q;
-  const __nv_bfloat16* __restrict__ a2 = kKeys ? args.v : args.dop;
-  const __nv_bfloat16* __restrict__ b1 = kKeys ? args.q : args.k;
-  const __nv_bfloat16* __restrict__ b2 = kKeys ? args.dop : args.v;
-  const float *nlse = args.nlse, *ndel = args.ndel;
-  const int words = args.words, k_max = args.k_max;
-  const int32_t *idx = args.idx, *counts = args.counts;
-  const uint32_t* mask = args.mask;
-  int32_t* status = args.status;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  __nv_bfloat16* A1 = reinterpret_cast<__nv_bfloat16*>(smem_raw);
-  __nv_bfloat16* A2 = A1 + kTileElems<D>;
-  __nv_bfloat16* Bs = A2 + kTileElems<D>;  // the stages of B1, B2
-  float* stats = reinterpret_cast<float*>(Bs + 2 * kStages<D> * kTileElems<D>);  // kKeys: [stage][-lse, -D][64]
-  const int t = blockIdx.x;  // this CTA's block of rows
-  const int64_t bh = blockIdx.y;
-  const int order = g.perm[(int)(bh % g.heads)];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int half = warp / 4, row_w = (warp % 4) * 16, c0 = half * 32;
-  const int64_t head = bh * g.Np, row = bh * g.NB + t;
-  const float scale_log2 = scale * kLog2e;
-
-  const int32_t* ids = kKeys ? nullptr : idx + row * k_max;
-  const uint32_t* bits = kKeys ? mask + row * words : nullptr;
-  fetch_tile<D>(A1, a1 + (head + t * kBlock) * D);
-  fetch_tile<D>(A2, a2 + (head + t * kBlock) * D);
-  int cnt = 0;
-  if constexpr (!kKeys) {
-    cnt = counts != nullptr ? __ldg(counts + row) : k_max;
-    if (!list_ok(ids, cnt, k_max, g.NB, lane)) {  // every warp alike
-      if (threadIdx.x == 0) report(status, PA_ERR_DEVICE_CHECK);
-      fetch_end();
-      fetch_wait<0>();
-      return;
-    }
-  }
-  // the tiles of the list in turn; -1 behind the last
-  int at = 0;
-  uint32_t left = 0;
-  auto next = [&]() -> int {
-    if constexpr (kKeys) {
-      while (left == 0) {
-        if (at >= words) return -1;
-        left = __ldg(bits + at++);
-      }
-      const int j = (at - 1) * 32 + __ffs(left) - 1;
-      left &= left - 1;
-      return j;
-    } else {
-      return at < cnt ? __ldg(ids + at++) : -1;
-    }
-  };
-  auto fetch = [&](int j, int stage) {
-    if (j >= 0) {
-      const int64_t rows = head + (int64_t)j * kBlock;
-      __nv_bfloat16* to = Bs + stage * 2 * kTileElems<D>;
-      fetch_tile<D>(to, b1 + rows * D);
-      fetch_tile<D>(to + kTileElems<D>, b2 + rows * D);
-      if (kKeys && threadIdx.x < 32) {
-        const float* src = (threadIdx.x < 16 ? nlse : ndel) + rows + (threadIdx.x % 16) * 4;
-        sm100::cp_async16(sm100::smem_u32(stats + stage * 2 * kBlock + threadIdx.x * 4), src, 16u);
-      }
-    }
-    fetch_end();
-  };
-  float nl[2] = {0.f, 0.f}, nd[2] = {0.f, 0.f};  // dQ: the rows' -lse, -D
-  if constexpr (!kKeys) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t r = head + t * kBlock + row_w + lane / 4 + 8 * u;
-      nl[u] = __ldg(nlse + r);
-      nd[u] = __ldg(ndel + r);
-    }
-  }
-  float acc1[D / 8][4], acc2[kKeys ? D / 8 : 1][4];
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      acc1[n][e] = 0.f;
-      if constexpr (kKeys) acc2[n][e] = 0.f;
-    }
-  int tiles[kStages<D>];  // this tile and those on their way
-#pragma unroll
-  for (int u = 0; u < kStages<D> - 1; ++u) {
-    tiles[u] = next();
-    fetch(tiles[u], u);  // the first with A1, A2
-  }
-  int stage = 0;
-  while (tiles[0] >= 0) {
-    const int j = tiles[0];
-    fetch_wait<kStages<D> - 2>();
-    // this tile is here for every warp, and the one before it is consumed
-    __syncthreads();
-    tiles[kStages<D> - 1] = next();
-    fetch(tiles[kStages<D> - 1], stage == 0 ? kStages<D> - 1 : stage - 1);
-    const __nv_bfloat16* B1 = Bs + stage * 2 * kTileElems<D>;
-    const __nv_bfloat16* B2 = B1 + kTileElems<D>;
-    float x[4][4], y[4][4];
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[nt][e] = y[nt][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ks += 2) {
-      uint32_t f1[2][4], f2[2][4];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        a_frag<D>(A1, row_w, ks + u, lane, f1[u]);
-        a_frag<D>(A2, row_w, ks + u, lane, f2[u]);
-      }
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        uint32_t b[4];
-        b_frag<D>(B1, c0 + nt * 8, ks, lane, b);
-        mma16816(x[nt], f1[0], b[0], b[1]);
-        mma16816(x[nt], f1[1], b[2], b[3]);
-        b_frag<D>(B2, c0 + nt * 8, ks, lane, b);
-        mma16816(y[nt], f2[0], b[0], b[1]);
-        mma16816(y[nt], f2[1], b[2], b[3]);
-      }
-    }
-    // x -> P, y -> dS; element e of an n-tile: row lane/4 + 8 (e / 2),
-    // column 2 (lane % 4) + e % 2
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const int col = c0 + nt * 8 + 2 * (lane % 4);
-      float2 cl, cd;
-      if constexpr (kKeys) {
-        cl = *reinterpret_cast<const float2*>(stats + stage * 2 * kBlock + col);
-        cd = *reinterpret_cast<const float2*>(stats + stage * 2 * kBlock + kBlock + col);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = kKeys ? (e & 1 ? cl.y : cl.x) : nl[e >> 1];
-        const float b = kKeys ? (e & 1 ? cd.y : cd.x) : nd[e >> 1];
-        float p = sm100::ex2(fmaf(x[nt][e], scale_log2, a));
-        if (!kKeys && j * kBlock + col + (e & 1) >= g.N) p = 0.f;  // pad keys
-        x[nt][e] = p;
-        y[nt][e] = p * (y[nt][e] + b);
-      }
-    }
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      uint32_t pa[4], sa[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int nt = 2 * ks + (u >> 1), e = 2 * (u & 1);
-        sa[u] = sm100::pack_bf16(y[nt][e], y[nt][e + 1]);
-        if constexpr (kKeys) pa[u] = sm100::pack_bf16(x[nt][e], x[nt][e + 1]);
-      }
-#pragma unroll
-      for (int n = 0; n < D / 8; n += 2) {
-        uint32_t b[4];
-        bt_frag<D>(B1, c0 + ks * 16, n * 8, lane, b);
-        mma16816(acc1[n], sa, b[0], b[1]);
-        mma16816(acc1[n + 1], sa, b[2], b[3]);
-        if constexpr (kKeys) {
-          bt_frag<D>(B2, c0 + ks * 16, n * 8, lane, b);
-          mma16816(acc2[n], pa, b[0], b[1]);
-          mma16816(acc2[n + 1], pa, b[2], b[3]);
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kStages<D> - 1; ++u) tiles[u] = tiles[u + 1];
-    stage = next_stage<D>(stage);
-  }
-  fetch_wait<0>();
-  auto finish = [&](float (&acc)[D / 8][4], float mul, __nv_bfloat16* dst) {
-    join<D>(acc, reinterpret_cast<float*>(Bs), half);
-    if (half == 0) stage_rows<D>(A1, acc, row_w, lane, mul);
-    __syncthreads();
-    store_rows<D>(A1, dst, g, order, bh, t);
-    __syncthreads();
-  };
-  __syncthreads();  // A1 may have come without a tile to wait for
-  finish(acc1, scale, kKeys ? args.dk : args.dq);
-  if constexpr (kKeys) finish(acc2, 1.f, args.dv);
-}
-
-// z = 0: the key blocks' CTAs, z = 1 the query blocks'.
-template <int D>
-__global__ void __launch_bounds__(kThreads)
-    bwd_mma_kernel(const __grid_constant__ BwdArgs args, const __grid_constant__ Grid g,
-                   float scale) {
-  if (blockIdx.z == 0)
-    bwd_block<D, true>(args, g, scale);
-  else
-    bwd_block<D, false>(args, g, scale);
-}
-
 template <int D>
 cudaError_t launch_fwd(const BwdArgs& a, const Grid& g, void* out, float* lse, cudaStream_t s) {
   const cudaError_t e = opt_in_smem<fwd_lse_kernel<D>>(kFwdSmem<D>);
@@ -503,24 +297,11 @@ cudaError_t launch_fwd(const BwdArgs& a, const Grid& g, void* out, float* lse, c
   return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_bwd(const BwdArgs& a, const Grid& g, cudaStream_t s) {
-  const cudaError_t e = opt_in_smem<bwd_mma_kernel<D>>(kBwdSmem<D>);
-  if (e != cudaSuccess) return e;
-  bwd_mma_kernel<D><<<dim3(g.NB, g.B * g.heads, 2), kThreads, kBwdSmem<D>, s>>>(
-      a, g, (float)(1.0 / sqrt((double)D)));
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_fwd_lse_mma(const BwdArgs& a, const Grid& g, void* out, float* lse,
                                cudaStream_t s) {
   return g.d == 64 ? launch_fwd<64>(a, g, out, lse, s) : launch_fwd<128>(a, g, out, lse, s);
-}
-
-cudaError_t launch_bwd_mma(const BwdArgs& a, const Grid& g, cudaStream_t s) {
-  return g.d == 64 ? launch_bwd<64>(a, g, s) : launch_bwd<128>(a, g, s);
 }
 
 }  // namespace paro
