@@ -22,22 +22,22 @@
 // pause.  (A CTA per block, which starts and ends 7 us around its tiles,
 // took 4 to 7% longer.)
 //
-// 12 warps:
-//   0-7    elementwise; warp w holds lanes 32 (w % 4) .. +31 (a row a
-//          thread) and the tile's columns 64 (w / 4) .. +63, so that two
-//          warps share each scheduler and the exponentials of one hide the
-//          tensor-memory loads of the other; at a block's end they read its
-//          sums and store them;
-//   8      tensor memory, and one lane that issues every MMA;
-//   9, 10  TMA loads of A1, A2, B1 and of B2;
-//   11     takes the blocks and hands them to the other warps, two ahead.
+// 20 warps:
+//   0-15    elementwise; warp w holds lanes 32 (w % 4) .. +31 (a row a
+//           thread) and the tile's columns 32 (w / 4) .. +31: four warps
+//           share a scheduler, and the exponentials of one hide the
+//           tensor-memory loads of the others; at a block's end they read
+//           its sums and store them;
+//   16      tensor memory, and one lane that issues every MMA;
+//   17, 18  TMA loads of A1, A2, B1 and of B2;
+//   19      takes the blocks and hands them to the other warps, two ahead.
 // The tiles of a CTA's blocks are numbered through (T below): stages and
 // barrier phases go on from block to block.
 // Tensor memory, 512 columns: kKeys at d = 128: X 0, Y 128, G1 256, G2 384;
 // otherwise three buffers at 0, 128, 256 that X and Y go round, G1 384 (and
 // kKeys, d = 64, G2 448).  A thread writes its P (or dS) as bf16 pairs over
-// the columns of X (or Y) that it read itself: 32 columns from column 64 g
-// of the buffer, g the column half.
+// the columns of X (or Y) that it read itself: 16 columns from column 32 g
+// of the buffer, g its part of the columns.
 // Issue order with one X and one Y (kKeys, d = 128): X0 Y0, then for every t:
 // G2(t) X(t+1) G1(t) Y(t+1): P(t+1) has the time of G1(t) and Y(t+1), dS(t)
 // that of G2(t) and X(t+1).  With three buffers: X0 Y0 X1, then (kKeys G2(t))
@@ -51,14 +51,14 @@
 // norm, against 0.0017 of rounding the result alone.  (dS as two bf16 halves
 // would bring it to the latter, for one more product a tile in each use.)
 //
-// Measured, d = 128: 196608 tiles in each use 4.18 ms, 1.38 PFLOP/s with the
+// Measured, d = 128: 196608 tiles in each use 4.16 ms, 1.39 PFLOP/s with the
 // products computed twice, at the clock that the power limit leaves (some
-// 1.7 GHz); 740 blocks of 12 tiles 234 us; d = 64, 2556 tiles 75 us.  Bounded
+// 1.7 GHz); 740 blocks of 12 tiles 235 us; d = 64, 2556 tiles 70 us.  Bounded
 // by the MMA stream and the power limit; with short lists by the gap between
 // two blocks (6000 cycles, of which the sums' way out is half; four warps of
-// their own for it gained 8 us of 240 there and lost 2% on long lists).  X in
-// two buffers and one Y: 4.24 ms, 241 us, 78 us.  16 elementwise warps changed
-// nothing.  The exponentials take 16384 / 16 = 1024 cycles a tile.
+// their own for it gained 8 us of 240 there and lost 2% on long lists).  With
+// 8 elementwise warps of 64 columns 4.23 ms, 236 us, 77 us; then with X in two
+// buffers and one Y 4.24 ms, 241 us, 78 us.
 // Waits are bounded as in the forward kernel.
 #include "bwd.cuh"
 #include "sm100.cuh"
@@ -71,9 +71,12 @@ using namespace sm100;
 
 constexpr int kBlock = 128;
 constexpr int kSms = 148;
-constexpr int kMmaWarp = 8, kB1Warp = 9, kB2Warp = 10, kItemWarp = 11;
-constexpr int kThreads = 12 * 32;
-constexpr int kAluThreads = 256;
+constexpr int kParts = 4;               // column parts of a tile, four elementwise warps each
+constexpr int kCols = 128 / kParts;     // a thread's columns of a tile
+constexpr int kAluWarps = 4 * kParts;
+constexpr int kMmaWarp = kAluWarps, kB1Warp = kAluWarps + 1, kB2Warp = kAluWarps + 2,
+              kItemWarp = kAluWarps + 3;
+constexpr int kThreads = (kAluWarps + 4) * 32;
 constexpr uint32_t kHalf = kBlock * 128;  // 64 columns of a tile: 16 KB
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOffBar = 0;      // two sets of NBAR barriers: kKeys, dQ
@@ -100,7 +103,7 @@ enum : uint32_t {
   NBAR = 26
 };
 static_assert(2 * NBAR * 8 <= kOffSlot, "barrier region");
-constexpr uint32_t kTakers = 8 + 2 + 1;  // elementwise warps, loaders, MMA
+constexpr uint32_t kTakers = kAluWarps + 2 + 1;  // elementwise warps, loaders, MMA
 
 // X and Y in three buffers that go round (X(T), Y(T), X(T + 1), Y(T + 1), ...)
 // for dQ, and for dK, dV at d = 64, where tensor memory has the room: the
@@ -115,6 +118,10 @@ template <int D>
 constexpr uint32_t kSmall =
     (kOffStats + kB1Stages<true, D> * 2 * kStatBytes + 1023) / 1024 * 1024;
 constexpr int kB2Stages = 2;
+
+// 32 or 16 columns of a thread's lane.
+__device__ __forceinline__ void tmem_cols(uint32_t at, uint32_t (&x)[32]) { tmem_ld32(at, x); }
+__device__ __forceinline__ void tmem_cols(uint32_t at, uint32_t (&x)[16]) { tmem_ld16(at, x); }
 
 // Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -288,12 +295,12 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
       }
     };
     // d += A B over the tile's 128 columns, A from the elementwise threads'
-    // pairs: columns 0-31 and 64-95 of the buffer at a
+    // pairs: the first half of each part's columns of the buffer at a
     auto gather = [&](uint32_t d, uint32_t a, uint64_t b, bool acc) {
 #pragma unroll
       for (int kk = 0; kk < kBlock / 16; ++kk)
-        mma_f16_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + (uint64_t)(kk * 128), id_g,
-                   (acc || kk > 0) ? 1u : 0u);
+        mma_f16_ts(d, a + (16 * kk / kCols) * kCols + (16 * kk % kCols) / 2,
+                   b + (uint64_t)(kk * 128), id_g, (acc || kk > 0) ? 1u : 0u);
     };
     auto b1_off = [&](uint32_t x) { return (uint64_t)((x % kS1) * (kTile >> 4)); };
     auto b2_off = [&](uint32_t x) { return (uint64_t)((x % kB2Stages) * (kTile >> 4)); };
@@ -377,11 +384,17 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
     __syncwarp();
   } else {
     // --------------------------------------------------- elementwise ----
-    const int half = warp >> 2;  // columns 64 half .. +63 of a tile
+    const int part = warp >> 2;  // columns kCols part .. + kCols - 1 of a tile
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t lane_addr = lanes + half * 64;
+    const uint32_t lane_addr = lanes + part * kCols;
+    // all lanes' tensor-memory writes and reads are behind the arrival
+    auto arrive = [&](uint32_t slot) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(slot));
+    };
     const float2 sc2 = make_float2(scale_log2, scale_log2);
     // the next block and, dQ, this thread's -lse and -D of it
     int row, next_n = 0;
@@ -411,21 +424,19 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
         tail = g.N - (g.NB - 1) * kBlock;
       for (int t = 0; t < n; ++t, ++T) {
         const float4* stat =
-            reinterpret_cast<const float4*>(smem + kOffStats + (T % kS1) * 2 * kStatBytes) + half * 16;
+            reinterpret_cast<const float4*>(smem + kOffStats + (T % kS1) * 2 * kStatBytes) +
+            part * (kCols / 4);
         if constexpr (kKeys)  // the statistics came with B1(T)
           if (!all_wait(bar(BB1 + T % kS1), (T / kS1) & 1, ctl)) { ok = false; break; }
         if (!warp_wait(bar(BX + (T & 1)), (T >> 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        uint32_t x[64], pk[32];
+        uint32_t x[kCols], pk[kCols / 2];
         const uint32_t x_col = lane_addr + col_x(T), y_col = lane_addr + col_y(T);
-        tmem_ld64(x_col, x);
-        if constexpr (!kKeys) {  // X is read: its buffer is free
-          tc_fence_before();
-          mbar_arrive(bar(BP + (T & 1)));
-        }
-        float2 p[32];
+        tmem_ld32(x_col, x);
+        if constexpr (!kKeys) arrive(BP + (T & 1));  // X is read: its buffer is free
+        float2 p[kCols / 2];
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
+        for (int c = 0; c < kCols / 2; c += 2) {
           float2 n0 = nl2, n1 = nl2;
           if constexpr (kKeys) {
             const float4 v = stat[c / 2];
@@ -441,23 +452,22 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
         }
         if constexpr (kKeys) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(p[c].x, p[c].y);
-          tmem_st32_async(x_col, pk);
+          for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16(p[c].x, p[c].y);
+          tmem_st16_async(x_col, pk);
           tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(BP + (T & 1)));
+          arrive(BP + (T & 1));
         } else if (tail < kBlock && t == n - 1) {  // warp-uniform: pad keys
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (half * 64 + 2 * c >= tail) p[c].x = 0.f;
-            if (half * 64 + 2 * c + 1 >= tail) p[c].y = 0.f;
+          for (int c = 0; c < kCols / 2; ++c) {
+            if (part * kCols + 2 * c >= tail) p[c].x = 0.f;
+            if (part * kCols + 2 * c + 1 >= tail) p[c].y = 0.f;
           }
         }
         if (!warp_wait(bar(BY + (T & 1)), (T >> 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld64(y_col, x);
+        tmem_ld32(y_col, x);
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
+        for (int c = 0; c < kCols / 2; c += 2) {
           float2 n0 = nd2, n1 = nd2;
           if constexpr (kKeys) {
             const float4 v = stat[kBlock / 4 + c / 2];
@@ -473,29 +483,29 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
           pk[c] = pack_bf16(s0.x, s0.y);
           pk[c + 1] = pack_bf16(s1.x, s1.y);
         }
-        tmem_st32_async(y_col, pk);
+        tmem_st16_async(y_col, pk);
         tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(BS + (T & 1)));
+        arrive(BS + (T & 1));
       }
       if (!ok) break;
       ahead();
-      // ---- the block's sums: column half `half` of this thread's row, as
-      // bf16 pairs in registers, then to the natural position of its token
-      constexpr int kPairs = D / 4;
+      // ---- the block's sums: this part's columns of the thread's row, as bf16
+      // pairs in registers, then to the natural position of its token
+      constexpr int kOut = D / kParts, kPairs = kOut / 2;
+      constexpr int kChunk = kOut < 32 ? kOut : 32;
       const int pos = blk * kBlock + r;
       const int64_t at =
           pos < g.N ? ((int64_t)bh * g.N + natural_index(g, g.perm[bh % g.heads], pos)) * D +
-                          half * (D / 2)
+                          part * kOut
                     : -1;
       uint32_t o1[kPairs], o2[kKeys ? kPairs : 1];
       auto sums = [&](uint32_t col, float mul, uint32_t (&o)[kPairs]) {
 #pragma unroll
-        for (int c0 = 0; c0 < D / 2; c0 += 32) {
-          uint32_t f[32];
-          tmem_ld32(lanes + col + half * (D / 2) + c0, f);
+        for (int c0 = 0; c0 < kOut; c0 += kChunk) {
+          uint32_t f[kChunk];
+          tmem_cols(lanes + col + part * kOut + c0, f);
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
+          for (int c = 0; c < kChunk / 2; ++c)
             o[c0 / 2 + c] =
                 pack_bf16(__uint_as_float(f[2 * c]) * mul, __uint_as_float(f[2 * c + 1]) * mul);
         }
@@ -508,8 +518,7 @@ __device__ __forceinline__ void bwd_blocks(const CUtensorMap& map_a1, const CUte
         tc_fence_after();
         sums(kColG1, scale, o1);
         if constexpr (kKeys) sums(kColG2, 1.f, o2);
-        tc_fence_before();
-        mbar_arrive(bar(BFREE));
+        arrive(BFREE);
       } else {
 #pragma unroll
         for (int c = 0; c < kPairs; ++c) {
@@ -558,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t set = 0; set < 2; ++set)
       for (uint32_t b = 0; b < NBAR; ++b)
         mbar_init(base + kOffBar + (set * NBAR + b) * 8u,
-                  b >= BP && b <= BFREE             ? kAluThreads
+                  b >= BP && b <= BFREE ? kAluWarps
                   : b == BTAKEN || b == BTAKEN + 1u ? kTakers
                                                     : 1);
     *abort_flag = 0;
