@@ -51,25 +51,28 @@ constexpr int kAluThreads = 256;
 constexpr uint32_t kOwnHalf = kBlock * 128;  // 64 columns of an own tile
 constexpr uint32_t kHalf = kStep * 128;      // of a streamed one; P or dS
 
+constexpr int kB1Stages = 3;  // X(t+1) is issued before G1(t), and G1(t) frees a stage
+
 enum : uint32_t {
   BA = 0,    // A1, A2 loaded
-  BB1 = 1,   // B1 stage full (2)
-  BB2 = 3,   // B2 stage full (2)
-  BX = 5,    // X(t) complete (ring of 2)
-  BY = 7,    // Y(t) complete (ring of 2)
-  BG1 = 9,   // G1(t) complete: its B1 stage (dQ: and B2 stage) and dS are free (2)
-  BG2 = 11,  // G2(t) complete: its B2 stage and P are free (2)
-  BP = 13,   // P(t) written by every elementwise thread (dQ: X(t) read)
-  BS = 14,   // dS(t) written
-  BDRAIN = 15,
-  NBAR = 16
+  BB1 = 1,   // B1 stage full (3)
+  BB2 = 4,   // B2 stage full (2)
+  BX = 6,    // X(t) complete (ring of 2)
+  BY = 8,    // Y(t) complete (ring of 2)
+  BG1 = 10,  // G1(t) complete: its B1 stage (dQ: and B2 stage) and dS are free (3)
+  BG2 = 13,  // G2(t) complete: its B2 stage and P are free (2)
+  BP = 15,   // P(t) written by every elementwise thread (dQ: X(t) read)
+  BS = 16,   // dS(t) written
+  BDRAIN = 17,
+  NBAR = 18
 };
 
 template <int D>
 struct Lay {
   static constexpr uint32_t kOwn = kBlock * D * 2, kTile = kStep * D * 2;
-  static constexpr uint32_t kA1 = 0, kA2 = kOwn, kB1 = 2 * kOwn, kB2 = kB1 + 2 * kTile,
-                            kP = kB2 + 2 * kTile, kS = kP + kHalf, kBar = kS + kHalf,
+  static constexpr uint32_t kA1 = 0, kA2 = kOwn, kB1 = 2 * kOwn, kB2 = kB1 + kB1Stages * kTile,
+                            kP = kB2 + 2 * kTile,  // P, then dS
+                            kBar = kP + kHalf,
                             kSlot = kBar + NBAR * 8,  // tensor memory's base, the abort flag
       kIds = kSlot + 8,                               // [stage][2]: the blocks of a step
       kStats = kIds + 24,                             // dQ: -lse, -D of the own rows
@@ -104,7 +107,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
     const bool first = warp == kB1Warp;
     const uint32_t ring = base + (first ? L::kB1 : L::kB2);
     const CUtensorMap* map = first ? &map_b1 : &map_b2;
-    const uint32_t full0 = first ? BB1 : BB2, free0 = kKeys && !first ? BG2 : BG1;
+    const uint32_t full0 = first ? BB1 : BB2;
     if (first && lane == 0) {
       mbar_arrive_tx(bar(BA), 2 * L::kOwn);
 #pragma unroll
@@ -134,11 +137,15 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
       }
     };
     int issued = 0;
+    const int stages = first ? kB1Stages : 2;
     for (int t = 0; t < n; ++t) {
-      const int s = t & 1;
+      const int s = t % stages;
       const bool two = 2 * t + 1 < cnt;
       const int j0 = entry(2 * t), j1 = two ? entry(2 * t + 1) : j0;
-      if (t >= 2 && !warp_wait(bar(free0 + s), ((t >> 1) - 1) & 1, ctl)) break;
+      const int last = t - stages;  // the step that had the stage
+      if (last >= 0 && !(kKeys && !first ? warp_wait(bar(BG2 + (last & 1)), (last >> 1) & 1, ctl)
+                                         : warp_wait(bar(BG1 + last % 3), (last / 3) & 1, ctl)))
+        break;
       if (lane == 0) {
         const uint32_t b = bar(full0 + s);
         if (first) {
@@ -158,8 +165,8 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
     // on every path this warp's copies have landed before it leaves
     if (lane == 0) {
       if (first) drain_phase(bar(BA), 0);
-      for (int t = issued > 2 ? issued - 2 : 0; t < issued; ++t)
-        drain_phase(bar(full0 + (t & 1)), (t >> 1) & 1);
+      for (int t = issued > stages ? issued - stages : 0; t < issued; ++t)
+        drain_phase(bar(full0 + t % stages), (t / stages) & 1);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -174,8 +181,8 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
       const uint64_t dm1 = sw128_desc(base + L::kB1, kHalf, 1024);  // MN-major
       const uint64_t dm2 = sw128_desc(base + L::kB2, kHalf, 1024);
       const uint64_t dp = sw128_desc(base + L::kP, kHalf, 1024);
-      const uint64_t ds = sw128_desc(base + L::kS, kHalf, 1024);
-      auto stage = [](int t) { return (uint64_t)((t & 1) * (L::kTile >> 4)); };
+      auto stage1 = [](int t) { return (uint64_t)(t % kB1Stages * (L::kTile >> 4)); };
+      auto stage2 = [](int t) { return (uint64_t)((t & 1) * (L::kTile >> 4)); };
       auto product = [&](uint32_t d, uint64_t b, uint64_t a) {  // d = B A^T over d
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
@@ -189,16 +196,16 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
                      (acc || kk > 0) ? 1u : 0u);
       };
       auto issue_x = [&](int t) -> bool {
-        if (!wait_phase(bar(BB1 + (t & 1)), (t >> 1) & 1, ctl)) return false;
+        if (!wait_phase(bar(BB1 + t % 3), (t / 3) & 1, ctl)) return false;
         tc_fence_after();
-        product(tmem + kColX, db1 + stage(t), da1);
+        product(tmem + kColX, db1 + stage1(t), da1);
         mma_commit(bar(BX + (t & 1)));
         return true;
       };
       auto issue_y = [&](int t) -> bool {
         if (!wait_phase(bar(BB2 + (t & 1)), (t >> 1) & 1, ctl)) return false;
         tc_fence_after();
-        product(tmem + kColY, db2 + stage(t), da2);
+        product(tmem + kColY, db2 + stage2(t), da2);
         mma_commit(bar(BY + (t & 1)));
         return true;
       };
@@ -209,15 +216,15 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
         tc_fence_after();
         if (t + 1 < n && !(ok = issue_x(t + 1))) break;
         if constexpr (kKeys) {
-          gather(tmem + kColG2, dp, dm2 + stage(t), t > 0);
+          gather(tmem + kColG2, dp, dm2 + stage2(t), t > 0);
           mma_commit(bar(BG2 + (t & 1)));
         }
         ok = wait_phase(bar(BS), t & 1, ctl);
         if (!ok) break;
         tc_fence_after();
         if (t + 1 < n && !(ok = issue_y(t + 1))) break;
-        gather(tmem + kColG1, ds, dm1 + stage(t), t > 0);
-        mma_commit(bar(BG1 + (t & 1)));
+        gather(tmem + kColG1, dp, dm1 + stage1(t), t > 0);
+        mma_commit(bar(BG1 + t % 3));
       }
       // every MMA issued above has completed once this commit fires
       mma_commit(bar(BDRAIN));
@@ -233,13 +240,12 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
     const float2 sc2 = make_float2(scale_log2, scale_log2);
     const float4* own = reinterpret_cast<const float4*>(smem + L::kStats) + 8 * half;
     uint4* p_row = reinterpret_cast<uint4*>(smem + L::kP + r * 128);
-    uint4* s_row = reinterpret_cast<uint4*>(smem + L::kS + r * 128);
     // the streamed row of step t: whether there is one, and (kKeys) its -lse, -D
     bool valid = false;
     float nl = 0.f, nd = 0.f;
     auto ahead = [&](int t) -> bool {
-      if (!all_wait(bar(BB1 + (t & 1)), (t >> 1) & 1, ctl)) return false;
-      const int j = step_ids[2 * (t & 1) + (r >> 6)];
+      if (!all_wait(bar(BB1 + t % 3), (t / 3) & 1, ctl)) return false;
+      const int j = step_ids[2 * (t % 3) + (r >> 6)];
       const int pos = j * kBlock + (r & 63);
       valid = j >= 0 && pos < g.N;
       if constexpr (kKeys) {
@@ -273,7 +279,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
         p[c + 1] = make_float2(ex2(e1.x), ex2(e1.y));
       }
       if constexpr (kKeys) {
-        if (t > 0 && !(ok = warp_wait(bar(BG2 + ((t - 1) & 1)), ((t - 1) >> 1) & 1, ctl))) break;
+        if (t > 0 && !(ok = warp_wait(bar(BG1 + (t - 1) % 3), ((t - 1) / 3) & 1, ctl))) break;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2* f = p + 4 * c;
@@ -287,7 +293,6 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
       mbar_arrive(bar(BP));
       if (t + 1 < n && !(ok = ahead(t + 1))) break;
       if (!(ok = warp_wait(bar(BY + (t & 1)), (t >> 1) & 1, ctl))) break;
-      if (t > 0 && !(ok = warp_wait(bar(BG1 + ((t - 1) & 1)), ((t - 1) >> 1) & 1, ctl))) break;
       tc_fence_after();
       tmem_ld32(lane_addr + kColY, x);
       uint32_t pk[16];
@@ -308,9 +313,13 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
         pk[c + 1] = pack_bf16(s1.x, s1.y);
         if (!kKeys && !was_valid) pk[c] = pk[c + 1] = 0u;  // (kKeys: P is 0 there)
       }
+      // the buffer is free once the product of P(t), or of dS(t - 1), is done
+      if (kKeys ? !(ok = warp_wait(bar(BG2 + (t & 1)), (t >> 1) & 1, ctl))
+                : t > 0 && !(ok = warp_wait(bar(BG1 + (t - 1) % 3), ((t - 1) / 3) & 1, ctl)))
+        break;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        s_row[(4 * half + c) ^ (r & 7)] =
+        p_row[(4 * half + c) ^ (r & 7)] =
             make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       fence_async_smem();
       tc_fence_before();
@@ -318,7 +327,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
     }
     // ---- the block's sums: row 16 (w % 4) + lane in lanes 0-15, column half w / 4
     if (ok && n > 0) {
-      ok = warp_wait(bar(BG1 + ((n - 1) & 1)), ((n - 1) >> 1) & 1, ctl);
+      ok = warp_wait(bar(BG1 + (n - 1) % 3), ((n - 1) / 3) & 1, ctl);
       if (kKeys && ok) ok = warp_wait(bar(BG2 + ((n - 1) & 1)), ((n - 1) >> 1) & 1, ctl);
       tc_fence_after();
     }
