@@ -12,8 +12,8 @@
 //   X = B1 A1^T (scores),  Y = B2 A2^T (dP)         128 x 64, from shared memory
 //   P = 2^(X c - lse),  dS = P o (Y - D)
 //   G1 += dS^T B1 (dK or dQ),  kKeys: G2 += P^T B2 (dV)   64 x d
-// P and dS go to shared memory as bf16, a row a thread, and are the
-// (M-major) A operand of the second products.  An odd list's last step holds
+// P and dS go to shared memory as bf16, one after the other into one buffer, a
+// row a thread, and are the (M-major) A operand of the second products.  An odd list's last step holds
 // its block twice, with P = dS = 0 in the second place: nothing but the
 // block's own kept tiles meets its sums, so what other rows hold (infinities,
 // NaN) stays there.
@@ -32,8 +32,10 @@
 //
 // Bounded by the chain X, P, Y, dS of a step; at d = 64 two CTAs share an SM
 // and fill each other's gaps.  Measured, d = 64: 307200 tiles in each use
-// 2.23 ms (mma.sync, which takes 4 times the tensor pipe's cycles: 4.72 ms);
-// 1280 tiles of 128 + 128 lists 22.7 us (29.4); the same at d = 128 30 us (51).
+// 2.00 ms (mma.sync, which takes 4 times the tensor pipe's cycles: 4.72 ms;
+// with a buffer each for P and dS and so only two stages of B1 2.23 ms);
+// 1280 tiles of 128 + 128 lists 22.5 us (29.4); the same at d = 128 31.5 us
+// (51), where one CTA fits an SM.
 #include "bwd.cuh"
 #include "sm100.cuh"
 
@@ -49,7 +51,7 @@ constexpr int kMmaWarp = 8, kB1Warp = 9;
 constexpr int kThreads = 11 * 32;
 constexpr int kAluThreads = 256;
 constexpr uint32_t kOwnHalf = kBlock * 128;  // 64 columns of an own tile
-constexpr uint32_t kHalf = kStep * 128;      // of a streamed one; P or dS
+constexpr uint32_t kHalf = kStep * 128;      // of a streamed one; P and dS
 
 constexpr int kB1Stages = 3;  // X(t+1) is issued before G1(t), and G1(t) frees a stage
 
@@ -144,7 +146,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
       const int j0 = entry(2 * t), j1 = two ? entry(2 * t + 1) : j0;
       const int last = t - stages;  // the step that had the stage
       if (last >= 0 && !(kKeys && !first ? warp_wait(bar(BG2 + (last & 1)), (last >> 1) & 1, ctl)
-                                         : warp_wait(bar(BG1 + last % 3), (last / 3) & 1, ctl)))
+                                         : warp_wait(bar(BG1 + last % kB1Stages), (last / kB1Stages) & 1, ctl)))
         break;
       if (lane == 0) {
         const uint32_t b = bar(full0 + s);
@@ -196,7 +198,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
                      (acc || kk > 0) ? 1u : 0u);
       };
       auto issue_x = [&](int t) -> bool {
-        if (!wait_phase(bar(BB1 + t % 3), (t / 3) & 1, ctl)) return false;
+        if (!wait_phase(bar(BB1 + t % kB1Stages), (t / kB1Stages) & 1, ctl)) return false;
         tc_fence_after();
         product(tmem + kColX, db1 + stage1(t), da1);
         mma_commit(bar(BX + (t & 1)));
@@ -224,7 +226,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
         tc_fence_after();
         if (t + 1 < n && !(ok = issue_y(t + 1))) break;
         gather(tmem + kColG1, dp, dm1 + stage1(t), t > 0);
-        mma_commit(bar(BG1 + t % 3));
+        mma_commit(bar(BG1 + t % kB1Stages));
       }
       // every MMA issued above has completed once this commit fires
       mma_commit(bar(BDRAIN));
@@ -244,8 +246,8 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
     bool valid = false;
     float nl = 0.f, nd = 0.f;
     auto ahead = [&](int t) -> bool {
-      if (!all_wait(bar(BB1 + t % 3), (t / 3) & 1, ctl)) return false;
-      const int j = step_ids[2 * (t % 3) + (r >> 6)];
+      if (!all_wait(bar(BB1 + t % kB1Stages), (t / kB1Stages) & 1, ctl)) return false;
+      const int j = step_ids[2 * (t % kB1Stages) + (r >> 6)];
       const int pos = j * kBlock + (r & 63);
       valid = j >= 0 && pos < g.N;
       if constexpr (kKeys) {
@@ -279,7 +281,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
         p[c + 1] = make_float2(ex2(e1.x), ex2(e1.y));
       }
       if constexpr (kKeys) {
-        if (t > 0 && !(ok = warp_wait(bar(BG1 + (t - 1) % 3), ((t - 1) / 3) & 1, ctl))) break;
+        if (t > 0 && !(ok = warp_wait(bar(BG1 + (t - 1) % kB1Stages), ((t - 1) / kB1Stages) & 1, ctl))) break;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2* f = p + 4 * c;
@@ -315,7 +317,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
       }
       // the buffer is free once the product of P(t), or of dS(t - 1), is done
       if (kKeys ? !(ok = warp_wait(bar(BG2 + (t & 1)), (t >> 1) & 1, ctl))
-                : t > 0 && !(ok = warp_wait(bar(BG1 + (t - 1) % 3), ((t - 1) / 3) & 1, ctl)))
+                : t > 0 && !(ok = warp_wait(bar(BG1 + (t - 1) % kB1Stages), ((t - 1) / kB1Stages) & 1, ctl)))
         break;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -327,7 +329,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
     }
     // ---- the block's sums: row 16 (w % 4) + lane in lanes 0-15, column half w / 4
     if (ok && n > 0) {
-      ok = warp_wait(bar(BG1 + (n - 1) % 3), ((n - 1) / 3) & 1, ctl);
+      ok = warp_wait(bar(BG1 + (n - 1) % kB1Stages), ((n - 1) / kB1Stages) & 1, ctl);
       if (kKeys && ok) ok = warp_wait(bar(BG2 + ((n - 1) & 1)), ((n - 1) >> 1) & 1, ctl);
       tc_fence_after();
     }
