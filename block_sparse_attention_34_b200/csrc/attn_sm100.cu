@@ -222,8 +222,8 @@ __device__ __forceinline__ void copy_tile(uint32_t tile, const __nv_bfloat16* __
 // head and are masked like the blocks past NB, rows past the array's end
 // read as zero).
 // D: 128, or 64 (permuted inputs, no compensation: the forward pass of
-// training).  lse, if not NULL, receives each row's log-sum-exp.
-template <bool kTma, bool kComp, int D = kD>
+// training).  kLse: lse receives each row's log-sum-exp.
+template <bool kTma, bool kComp, int D = kD, bool kLse = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_sm100_kernel(const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_k,
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // that test failed.
       // (Not an elected lane at d = 64: its products are half as long, and
       // issued without a pause they bring the two groups' tiles at once:
-      // 24 tiles a block took 108 us instead of 95.)
+      // 24 tiles a block took 100 us instead of 88.)
       if (n_tiles > 0 && (kD == 64 ? lane == 0 : elect_one())) {
         constexpr uint32_t id_qk = idesc_bf16(kBlock, kBlock, false);
         constexpr uint32_t id_pv = idesc_bf16(kBlock, kD, true);
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t nat = p < g.N ? bh * (int64_t)g.N + natural_index(g, order, p) : -1;
     __nv_bfloat16* orow = nat >= 0 ? out + nat * kD : nullptr;
     if (run && n_tiles == 0) {
-      if (lse != nullptr && nat >= 0 && grp == 0) lse[nat] = -INFINITY;
+      if (kLse && nat >= 0 && grp == 0) lse[nat] = -INFINITY;
       if (orow != nullptr)
         for (int c = 0; c < kD / 16; ++c)
           reinterpret_cast<uint4*>(orow + grp * (kD / 2))[c] = make_uint4(0, 0, 0, 0);
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lt = (m0 == -INFINITY ? 0.f : lsum[r] * ex2(m0 - m)) +
                          (m1 == -INFINITY ? 0.f : lsum[128 + r] * ex2(m1 - m));
         inv = lt > 0.f ? 1.f / lt : 0.f;
-        if (lse != nullptr && nat >= 0 && grp == 0) lse[nat] = row_lse(m, lt);
+        if (kLse && nat >= 0 && grp == 0) lse[nat] = row_lse(m, lt);
       }
       // every P V has completed once the last one's commit fired
       if (okm) okm = warp_wait(pv_done(n_tiles - 1), ring_par(n_tiles - 1), ctl);
@@ -753,8 +753,8 @@ cudaError_t launch_typed(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
 template <int D>
 cudaError_t launch_lse(const BwdArgs& a, const Grid& g, void* out, float* lse, cudaStream_t s) {
   constexpr int kSmem = kOffQ + (1 + 2 * kStages) * kBlock * D * 2;
-  auto kern = attn_sm100_kernel<true, false, D>;
-  const cudaError_t e = opt_in_smem<attn_sm100_kernel<true, false, D>>(kSmem);
+  auto kern = attn_sm100_kernel<true, false, D, true>;
+  const cudaError_t e = opt_in_smem<attn_sm100_kernel<true, false, D, true>>(kSmem);
   if (e != cudaSuccess) return e;
   const uint64_t rows = (uint64_t)g.B * g.heads * g.Np;
   CUtensorMap mq{}, mk{}, mv{}, none{};

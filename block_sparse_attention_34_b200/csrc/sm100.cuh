@@ -123,8 +123,8 @@ __device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, Ctl c) {
 // One lane of a converged warp, the one that issues its MMAs.  (Under
 // `lane == 0` the compiler does not know that one lane is left and guards
 // every MMA's operands, some 95 cycles an instruction, more than the 64 that
-// a 128 x 128 x 16 one takes: the attention over 2.1 M kept tiles took 17.6
-// ms so, and 15.9 ms with this.)
+// a 128 x 128 x 16 one takes: the attention over 2.1 M kept tiles took 17.8
+// ms so, and 15.5 ms with this.)
 __device__ __forceinline__ bool elect_one() {
   uint32_t leader;
   asm volatile(
