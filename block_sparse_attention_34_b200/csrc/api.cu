@@ -655,7 +655,7 @@ pa_status pa_block_sparse_attn_lse(const void* q, const void* k, const void* v, 
     a.k_max = k_max;
     a.status = dev_status;
     e = g.block == 128 ? paro::launch_fwd_lse_sm100(a, g, out, lse, s)
-                       : paro::launch_fwd_lse_mma(a, g, out, lse, s);
+                       : paro::launch_fwd64_sm100(a, g, out, lse, s);
   }
   return cuda_status(e, "pa_block_sparse_attn_lse launch");
 }

@@ -62,15 +62,14 @@ __device__ __forceinline__ bool list_ok(const int32_t* __restrict__ ids, int cnt
 
 cudaError_t launch_bwd_prep(const void* out, const void* dout, const float* lse,
                             const float* dlse, const BwdArgs& a, const Grid& g, cudaStream_t s);
-// The tcgen05 kernels of block 128 (attn_sm100.cu, attn_bwd_sm100.cu); of
-// block 64 the warp-level forward pass (attn_fwd64_mma.cu) and the tcgen05
-// backward one (attn_bwd64_sm100.cu).  Of the arguments the forward pass uses
-// q, k, v, idx, counts, k_max and status.
+// The kernels of block 128 (attn_sm100.cu, attn_bwd_sm100.cu) and of block 64
+// (attn_fwd64_sm100.cu, attn_bwd64_sm100.cu).  Of the arguments the forward
+// pass uses q, k, v, idx, counts, k_max and status.
 cudaError_t launch_fwd_lse_sm100(const BwdArgs& a, const Grid& g, void* out, float* lse,
                                  cudaStream_t s);
 cudaError_t launch_bwd_sm100(const BwdArgs& a, const Grid& g, cudaStream_t s);
 cudaError_t launch_bwd64_sm100(const BwdArgs& a, const Grid& g, cudaStream_t s);
-cudaError_t launch_fwd_lse_mma(const BwdArgs& a, const Grid& g, void* out, float* lse,
+cudaError_t launch_fwd64_sm100(const BwdArgs& a, const Grid& g, void* out, float* lse,
                                cudaStream_t s);
 
 }  // namespace paro

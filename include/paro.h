@@ -476,8 +476,8 @@ PA_API pa_status pa_rope_reorder(const void* x, const int64_t* x_stride, void* x
  * [B,heads,N_p,d] (pa_reorder's or pa_rope_reorder's output, pad rows zero),
  * which also stores lse[b,h,n] = log sum_c exp(q_n . k_c / sqrt(d)) over the
  * row's kept keys (natural log; [B,heads,N] float, natural order; -inf for a
- * row without kept blocks).  Block 128 runs on the tcgen05 kernel (d = 128:
- * out equals pa_block_sparse_attn's bit for bit), block 64 on mma.sync.
+ * row without kept blocks).  At block 128 and d = 128 out equals
+ * pa_block_sparse_attn's bit for bit.
  * NB <= 65535, B * heads <= 65535, B * heads * N_p < 2^31. */
 PA_API pa_status pa_block_sparse_attn_lse(const void* q, const void* k, const void* v,
                                           pa_dtype dtype, pa_shape shape, const int8_t* perms,
