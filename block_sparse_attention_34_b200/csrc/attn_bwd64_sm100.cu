@@ -18,13 +18,12 @@
 // block's own kept tiles meets its sums, so what other rows hold (infinities,
 // NaN) stays there.
 //
-// 11 warps:
+// 10 warps:
 //   0-7  elementwise: warp w holds the streamed rows 32 (w % 4) .. +31 (a row
 //        a thread) and the columns 32 (w / 4) .. +31 of X and Y; at the end
 //        the sums' rows;
 //   8    tensor memory, and one lane that issues every MMA;
-//   9    TMA loads of A1, A2 and B1, and which blocks a step holds;
-//   10   of B2.
+//   9    TMA loads, and which blocks a step holds.
 // Tensor memory: X 0, Y 64, G1 128, G2 128 + d.  The 64 rows of a sum are in
 // lanes 32 w + 0..15, w = 0..3.
 // Issue order: X0 Y0, then for every t: X(t+1), (kKeys) G2(t) once P(t) is
@@ -32,10 +31,10 @@
 //
 // Bounded by the chain X, P, Y, dS of a step; at d = 64 two CTAs share an SM
 // and fill each other's gaps.  Measured, d = 64: 307200 tiles in each use
-// 2.00 ms (mma.sync, which takes 4 times the tensor pipe's cycles: 4.72 ms;
-// with a buffer each for P and dS and so only two stages of B1 2.23 ms);
-// 1280 tiles of 128 + 128 lists 22.5 us (29.4); the same at d = 128 31.5 us
-// (51), where one CTA fits an SM.
+// 1.95 ms (mma.sync, which takes 4 times the tensor pipe's cycles: 4.72 ms;
+// two load warps, which leave 80 registers: 2.00; with a buffer each for P and
+// dS and so only two stages of B1 2.23); 1280 tiles of 128 + 128 lists 21.3 us
+// (29.4); the same at d = 128 30.9 us (51), where one CTA fits an SM.
 #include "bwd.cuh"
 #include "sm100.cuh"
 
@@ -47,8 +46,8 @@ using namespace sm100;
 
 constexpr int kBlock = 64;
 constexpr int kStep = 128;
-constexpr int kMmaWarp = 8, kB1Warp = 9;
-constexpr int kThreads = 11 * 32;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 10 * 32;  // 96 registers a thread with two CTAs on an SM
 constexpr int kAluThreads = 256;
 constexpr uint32_t kOwnHalf = kBlock * 128;  // 64 columns of an own tile
 constexpr uint32_t kHalf = kStep * 128;      // of a streamed one; P and dS
@@ -104,13 +103,9 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
   const int n = (cnt + 1) / 2;  // steps
   volatile int32_t* step_ids = reinterpret_cast<int32_t*>(smem + L::kIds);
 
-  if (warp >= kB1Warp) {
+  if (warp == kLoadWarp) {
     // -------------------------------------------------------- copies ----
-    const bool first = warp == kB1Warp;
-    const uint32_t ring = base + (first ? L::kB1 : L::kB2);
-    const CUtensorMap* map = first ? &map_b1 : &map_b2;
-    const uint32_t full0 = first ? BB1 : BB2;
-    if (first && lane == 0) {
+    if (lane == 0) {
       mbar_arrive_tx(bar(BA), 2 * L::kOwn);
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
@@ -138,37 +133,43 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
         return __shfl_sync(0xffffffffu, id_lane, e & 31);
       }
     };
-    int issued = 0;
-    const int stages = first ? kB1Stages : 2;
+    auto load = [&](const CUtensorMap* map, uint32_t to, int j0, int j1, uint32_t b) {
+      mbar_arrive_tx(b, L::kTile);  // release: the ids are visible behind the barrier
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        tma_load_2d(to + h * kHalf, map, 64 * h, head + j0 * kBlock, b);
+        tma_load_2d(to + h * kHalf + kOwnHalf, map, 64 * h, head + j1 * kBlock, b);
+      }
+    };
+    auto g1_done = [&](int t) {
+      return t < 0 || warp_wait(bar(BG1 + t % kB1Stages), (t / kB1Stages) & 1, ctl);
+    };
+    int issued1 = 0, issued2 = 0;
     for (int t = 0; t < n; ++t) {
-      const int s = t % stages;
+      const int s1 = t % kB1Stages, s2 = t & 1;
       const bool two = 2 * t + 1 < cnt;
       const int j0 = entry(2 * t), j1 = two ? entry(2 * t + 1) : j0;
-      const int last = t - stages;  // the step that had the stage
-      if (last >= 0 && !(kKeys && !first ? warp_wait(bar(BG2 + (last & 1)), (last >> 1) & 1, ctl)
-                                         : warp_wait(bar(BG1 + last % kB1Stages), (last / kB1Stages) & 1, ctl)))
-        break;
+      if (!g1_done(t - kB1Stages)) break;
       if (lane == 0) {
-        const uint32_t b = bar(full0 + s);
-        if (first) {
-          step_ids[2 * s] = j0;
-          step_ids[2 * s + 1] = two ? j1 : -1;
-        }
-        mbar_arrive_tx(b, L::kTile);  // release: the ids are visible behind the barrier
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          const uint32_t to = ring + s * L::kTile + h * kHalf;
-          tma_load_2d(to, map, 64 * h, head + j0 * kBlock, b);
-          tma_load_2d(to + kOwnHalf, map, 64 * h, head + j1 * kBlock, b);
-        }
+        step_ids[2 * s1] = j0;
+        step_ids[2 * s1 + 1] = two ? j1 : -1;
+        load(&map_b1, base + L::kB1 + s1 * L::kTile, j0, j1, bar(BB1 + s1));
       }
-      issued = t + 1;
+      issued1 = t + 1;
+      const int last = t - 2;  // the step that had the B2 stage
+      if (!(kKeys ? last < 0 || warp_wait(bar(BG2 + (last & 1)), (last >> 1) & 1, ctl)
+                  : g1_done(last)))
+        break;
+      if (lane == 0) load(&map_b2, base + L::kB2 + s2 * L::kTile, j0, j1, bar(BB2 + s2));
+      issued2 = t + 1;
     }
     // on every path this warp's copies have landed before it leaves
     if (lane == 0) {
-      if (first) drain_phase(bar(BA), 0);
-      for (int t = issued > stages ? issued - stages : 0; t < issued; ++t)
-        drain_phase(bar(full0 + t % stages), (t / stages) & 1);
+      drain_phase(bar(BA), 0);
+      for (int t = issued1 > kB1Stages ? issued1 - kB1Stages : 0; t < issued1; ++t)
+        drain_phase(bar(BB1 + t % kB1Stages), (t / kB1Stages) & 1);
+      for (int t = issued2 > 2 ? issued2 - 2 : 0; t < issued2; ++t)
+        drain_phase(bar(BB2 + (t & 1)), (t >> 1) & 1);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
