@@ -182,6 +182,23 @@ def test_nan_stays_in_its_rows(block, d):
         assert t[:, :, block:2 * block].isnan().any()
 
 
+@pytest.mark.parametrize("block,d", [(128, 128), (128, 64), (64, 128), (64, 64)])
+@pytest.mark.parametrize("up", [True, False], ids=["growing", "falling"])
+def test_scores_that_grow_or_fall_along_the_list(block, d, up):
+    """The running reference of a row moves at most steps, or at the first alone."""
+    nb = -(-4 * 10 * 13 // block)
+    c = Case(B=1, heads=2, d=d, block=block, grid=(4, 10, 13), orders=(0, 3), k=nb)
+    steps = torch.linspace(-2, 3, nb).round().exp2()  # powers of two: exact in bf16
+    steps = (steps if up else steps.flip(0)).to("cuda", BF)
+    kp = c.perm[1].view(1, 2, nb, block, d) * steps[:, None, None]
+    c.perm[1] = kp.view(c.pr.permuted)
+    c.k = paro.inverse_reorder(c.perm[1], c.pr)
+    out, lse = c.forward()
+    grads = c.backward(out, lse, c.dlse)
+    want, bounds = c.oracle(c.dlse)
+    check(dict(zip(NAMES, (out, lse, *grads))), want, bounds)
+
+
 def test_difference_along_a_direction():
     """The kernels' gradients against differences of the oracle's loss."""
     c = Case(**CASES["d64_b128_ragged"])
