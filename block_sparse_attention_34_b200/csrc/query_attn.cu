@@ -20,14 +20,16 @@
 //
 // bf16: the products run on mma.sync m16n8k16 with the query rows as rows of
 // the tile (the scalar form, 16 lanes a key, took four times the
-// instructions and held a CTA at 46 GB/s).  Measured: 12 heads' one row over 64
-// of 256 blocks (52 MB) 17.5 us, of which some 9 are the launch, the scores'
-// latency and the join, the rest at 6.5 TB/s; 40 heads' 16 rows each over 89
-// of 591 blocks (1.56 GB read once) 275 us, 5.7 TB/s.  P is not rounded to bf16 but
+// instructions and held a CTA at 46 GB/s).  P is not rounded to bf16 but
 // split, p = bf16(p) + rest, and both parts multiply V, so P V keeps 16 bits
 // of P: up to 8 query rows sit in rows 0-7 of the tile and the rests in rows
 // 8-15; with more, the rests are a second product.  fp32: one row a cluster,
 // fp32 arithmetic throughout.
+//
+// Measured: 12 heads' one row over 64 of 256 blocks (52 MB) 17.5 us, of which
+// some 9 are the launch, the scores' latency and the join, the rest at 6.5
+// TB/s; 40 heads' 16 rows each over 89 of 591 blocks (1.56 GB, each block read
+// once) 272 us, 5.7 TB/s.
 #include <type_traits>
 
 #include "bwd.cuh"

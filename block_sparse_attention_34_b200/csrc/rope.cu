@@ -251,8 +251,8 @@ struct Unit {
 };
 
 // x -> y, any strides of batch, head and token.  A thread owns one unit of
-// one token and goes over `per` heads with it, at most kHeads: the table is read once for
-// them, and all their loads are in flight before the first store.  Rows of
+// one token and goes over `per` heads with it, at most kHeads: the table is
+// read once for them, and all their loads are in flight before the first store.  Rows of
 // 16 (or 32) tokens of a head are neighbours in a head-major tensor, rows of
 // kHeads heads of a token in a token-major one: both sides move whole
 // kilobytes.  Bound by HBM: 40 heads of 75,600 bf16 tokens take 233 us (6.6
