@@ -560,9 +560,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const int warp = threadIdx.x >> 5;
   const Ctl ctl{abort_flag, status, kTimeoutNs};
-  // a wait of an earlier launch already expired: end quickly
-  const bool expired =
-      status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT;
+  // a wait of an earlier launch already expired: end quickly, with one answer
+  // for the CTA: the status may change between its threads' reads
+  if (__syncthreads_or(status != nullptr &&
+                       *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT))
+    return;
   if (threadIdx.x == 0) {
     for (uint32_t set = 0; set < 2; ++set)
       for (uint32_t b = 0; b < NBAR; ++b)
@@ -578,16 +580,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (!expired) {
-    bwd_blocks<true, D>(map_k, map_v, map_q, map_do, args, g, scale, scale_log2, smem_raw, base,
-                        tmem, ctl);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (*abort_flag == 0)
-      bwd_blocks<false, D>(map_q, map_do, map_k, map_v, args, g, scale, scale_log2, smem_raw, base,
-                           tmem, ctl);
-  }
+  bwd_blocks<true, D>(map_k, map_v, map_q, map_do, args, g, scale, scale_log2, smem_raw, base, tmem,
+                      ctl);
+  tc_fence_before();
+  const bool aborted = __syncthreads_or(*abort_flag != 0);
+  tc_fence_after();
+  if (!aborted)
+    bwd_blocks<false, D>(map_q, map_do, map_k, map_v, args, g, scale, scale_log2, smem_raw, base,
+                         tmem, ctl);
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {

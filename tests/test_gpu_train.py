@@ -327,3 +327,22 @@ def test_the_480p_layer_on_sampled_rows():
         sv += (p[valid][:, cols]).T @ D[valid]
     near(dk[0, h, j * 128:(j + 1) * 128], sk)
     near(dv[0, h, j * 128:(j + 1) * 128], sv)
+
+
+@pytest.mark.parametrize("block,d", [(128, 128), (128, 64), (64, 128), (64, 64)])
+def test_an_expired_status_ends_every_pass(block, d):
+    """A status word that already records PA_ERR_TIMEOUT: forward and backward
+    return at once, write nothing and leave it as it was; a normal call
+    follows on the cleared word."""
+    c = Case(2, 3, d, block, (5, 16, 17), (0, 3, 5), 3, counts="random")
+    out, lse = c.forward()
+    want = c.backward(out, lse, c.dlse)
+    status = torch.full((1,), paro.PA_ERR_TIMEOUT, dtype=torch.int32, device="cuda")
+    ended = (*c.forward(status=status), *c.backward(out, lse, c.dlse, status=status))
+    assert status.item() == paro.PA_ERR_TIMEOUT
+    assert all(t.isnan().all() for t in ended)
+    paro.clear_status(status)
+    for a, b in zip((*c.forward(status=status), *c.backward(out, lse, c.dlse, status=status)),
+                    (out, lse, *want)):
+        assert torch.equal(a, b)
+    assert status.item() == 0
