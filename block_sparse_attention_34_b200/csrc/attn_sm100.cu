@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kOffSlot);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* bad_flag = tmem_slot + 2;
+  volatile uint32_t* expired_flag = tmem_slot + 3;
   float* lsum = reinterpret_cast<float*>(gbase + kOffMerge);  // [group][row]
   float* mref = reinterpret_cast<float*>(gbase + kOffRef);    // [group][row]
   auto bar = [&](uint32_t slot) { return base + kOffBar + slot * 8u; };
@@ -269,10 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t* ids = idx + row * k_max;
   const int cnt = counts != nullptr ? __ldg(counts + row) : k_max;
   const Ctl ctl{abort_flag, status, st.limit_ns};
-  // a wait of an earlier CTA of this launch already expired: end quickly
-  const bool expired =
-      status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT;
-
   if (threadIdx.x == 0) {
     constexpr uint32_t kLoadArrivals = kTma ? 1 : 32;  // one expect-tx, or one per lane
     mbar_init(bar(BQ), kLoadArrivals);
@@ -292,12 +289,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(BDRAIN), 1);
     mbar_init(bar(BM), 2 * kGroupThreads);
     *abort_flag = 0;
-    *bad_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   if (warp == kPvWarp) {
-    // the kept list: count in range, indices ascending in [0, NB)
+    // Whether this CTA skips its work, said by this warp alone so that every
+    // thread has the same answer: a malformed kept list (count in range,
+    // indices ascending in [0, NB)), or a wait of an earlier CTA or launch that
+    // already expired (the status may change between two threads' reads).  In
+    // two words: with one, the softmax loop spills
     bool bad = cnt < 0 || cnt > k_max;
     if (!bad) {
       for (int e = lane; e < cnt; e += 32) {
@@ -306,15 +306,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         bad |= (j <= prev) || (j >= g.NB);
       }
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) {
-      *bad_flag = 1;
-      report(status, PA_ERR_DEVICE_CHECK);
+    const bool malformed = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      *bad_flag = malformed;
+      *expired_flag =
+          status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT;
+      if (malformed) report(status, PA_ERR_DEVICE_CHECK);
     }
     if constexpr (kComp) {
       uint32_t* bits = reinterpret_cast<uint32_t*>(gbase + kOffBits);
       for (int x = lane; x < kCompMaxNB / 32; x += 32) bits[x] = 0u;
       __syncwarp();
-      if (!__any_sync(0xffffffffu, bad))  // a malformed list is never used
+      if (!malformed)  // a malformed list is never used
         for (int e = lane; e < cnt; e += 32) {
           const int jb = __ldg(ids + e);
           atomicOr(bits + (jb >> 5), 1u << (jb & 31));
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const bool run = *bad_flag == 0 && !expired;
+  const bool run = *bad_flag == 0 && *expired_flag == 0;
   const int n_pool = kComp ? (g.NB + kBlock - 1) / kBlock : 0;  // pooled tiles
   const int n_tiles = run ? cnt + n_pool : 0;
   const __nv_bfloat16* qh = q + bh * (int64_t)g.N * kD;

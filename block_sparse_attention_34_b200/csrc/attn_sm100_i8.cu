@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + kOffSlot);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* bad_flag = tmem_slot + 2;
+  volatile uint32_t* expired_flag = tmem_slot + 3;
   float* xch = reinterpret_cast<float*>(smem_raw + kOffX);
   float* s_alpha = reinterpret_cast<float*>(smem_raw + kOffA);
   float* s_cv = reinterpret_cast<float*>(smem_raw + kOffC);
@@ -228,8 +229,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t* ids = idx + row * k_max;
   const int cnt = counts != nullptr ? __ldg(counts + row) : k_max;
   Ctl ctl{abort_flag, status};
-  const bool expired =
-      status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT;
 
   if (threadIdx.x == 0) {
     mbar_init(bar(BQ), 1);
@@ -253,11 +252,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(BMG), kSoftThreads);
     for (int b = 0; b < 2; ++b) mbar_init(bar(BAM0 + b), kSoftWarps);
     *abort_flag = 0;
-    *bad_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   if (warp == kLoadWarp) {
+    // whether this CTA skips its work (a malformed kept list, or a wait that
+    // already expired), said by this warp alone: one answer for the CTA
     bool bad = cnt < 0 || cnt > k_max;
     if (!bad) {
       for (int e = lane; e < cnt; e += 32) {
@@ -266,16 +266,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         bad |= (j <= prev) || (j >= g.NB);
       }
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) {
-      *bad_flag = 1;
-      report(status, PA_ERR_DEVICE_CHECK);
+    const bool malformed = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      *bad_flag = malformed;
+      *expired_flag =
+          status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT;
+      if (malformed) report(status, PA_ERR_DEVICE_CHECK);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const bool run = *bad_flag == 0 && !expired;
+  const bool run = *bad_flag == 0 && *expired_flag == 0;
   const int n_tiles = run ? cnt : 0;
   const int row0 = (int)(bh * g.Np);
 

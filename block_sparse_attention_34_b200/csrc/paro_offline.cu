@@ -88,8 +88,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t bh = blockIdx.y;
   const int nb = g.NB;
   Ctl ctl{abort_flag, status};
-  const bool expired =
-      status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT;
+  // one answer for the CTA: the status may change between its threads' reads
+  const bool expired = __syncthreads_or(
+      status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT);
 
   if (threadIdx.x == 0) {
     mbar_init(bar(BQ), 1);

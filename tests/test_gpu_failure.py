@@ -61,3 +61,32 @@ def test_bounded_wait_runs_out_and_context_stays_usable(permuted):
     assert status.item() == 0
     compare(out, want)
 
+
+
+@pytest.mark.parametrize("form", ["tma_tiles", "gathered_rows", "compensated", "int8", "int8_p_tile", "map"])
+def test_an_expired_status_ends_the_launch(form):
+    """A status word that already records PA_ERR_TIMEOUT: every kernel with
+    bounded waits returns at once, writes nothing and leaves the word."""
+    pr = paro.Problem(1, 3, (5, 16, 17), 128, 128, [0, 3, 5])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    x = torch.randn(pr.natural, generator=g, device="cuda").bfloat16()
+    xp, pool = paro.reorder(x, pr, with_pool=True)
+    idx = torch.arange(pr.NB, dtype=torch.int32, device="cuda").expand(pr.square).contiguous()
+    status = torch.full((1,), paro.PA_ERR_TIMEOUT, dtype=torch.int32, device="cuda")
+    out = torch.full(pr.natural, float("nan"), dtype=torch.bfloat16, device="cuda")
+    if form == "tma_tiles":
+        paro.block_sparse_attn(xp, xp, xp, pr, idx, out=out, status=status, permuted=True)
+    elif form == "gathered_rows":
+        paro.block_sparse_attn(x, x, x, pr, idx, out=out, status=status)
+    elif form == "compensated":
+        paro.block_sparse_attn_compensated(xp, xp, xp, pr, idx[..., :2].contiguous(), pool, pool, out=out,
+                                           status=status, permuted=True)
+    elif form == "map":
+        paro.map_row_stats(xp, xp, pr, 0, status)
+    else:
+        x8, scale = paro.quantize_int8(x, pr)
+        paro.block_sparse_attn(x8, x8, x8, pr, idx, scales=(scale,) * 3, out=out, status=status,
+                               p_tile=form == "int8_p_tile")
+    assert status.item() == paro.PA_ERR_TIMEOUT
+    assert out.isnan().all()
