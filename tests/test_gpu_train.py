@@ -346,3 +346,61 @@ def test_an_expired_status_ends_every_pass(block, d):
                     (out, lse, *want)):
         assert torch.equal(a, b)
     assert status.item() == 0
+
+
+def many_blocks(d, block, seed):
+    """600 blocks of 40 heads, more than four for each CTA of the persistent
+    backward kernel, whose lists have 0 to 7 entries, with runs of lists of
+    none and of one and a head without any."""
+    c = Case(1, 40, d, block, (5, 19, 4 * block // 25), [h % 12 for h in range(40)], 7, counts="random", seed=seed)
+    n = c.counts_np.reshape(-1)
+    assert n.size >= 4 * 148
+    n[90:130] = 0
+    n[300:340] = 1
+    n[450:470] = np.arange(20) % 2
+    c.counts_np[0, 33] = 0
+    c.counts = torch.from_numpy(c.counts_np).cuda()
+    return c
+
+
+@pytest.mark.parametrize("block,d", [(128, 128), (128, 64), (64, 64)])
+def test_many_blocks_of_many_lengths(block, d):
+    c = many_blocks(d, block, 11)
+    out, lse = c.forward()
+    grads = c.backward(out, lse, c.dlse)
+    want, bounds = c.oracle(c.dlse)
+    check(dict(zip(NAMES, (out, lse, *grads))), want, bounds)
+    for _ in range(6):  # whichever CTA takes a block
+        for a, b in zip(c.backward(out, lse, c.dlse), grads):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("block,d", [(128, 128), (128, 64), (64, 64)])
+def test_malformed_lists_among_many_blocks(block, d):
+    """They add nothing and their rows of dq stay as they were; every other
+    block's sums are as if they kept nothing."""
+    c = many_blocks(d, block, 12)
+    bad = [(0, 1), (0, 2), (7, 0), (13, 5), (13, 6), (13, 7), (30, 14), (39, 14)]
+    for h, i in bad:
+        c.counts_np[0, h, i] = 0
+    c.counts = torch.from_numpy(c.counts_np).cuda()
+    out, lse = c.forward()
+    want, bounds = c.oracle()
+    for n, (h, i) in enumerate(bad):
+        c.idx[0, h, i] = torch.arange(7, dtype=torch.int32)
+        c.idx[0, h, i, 1] = (0, c.pr.NB, -1, 2)[n % 4]
+        c.counts[0, h, i] = (7, 3)[n % 2] if n != 5 else 8  # 8: more entries than there are
+    rows = torch.zeros(c.pr.permuted, dtype=BF, device="cuda")
+    for h, i in bad:
+        rows[0, h, i * block:(i + 1) * block] = 1
+    rows = paro.inverse_reorder(rows, c.pr)[..., 0] == 1
+    first = None
+    for _ in range(4):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        dq, dk, dv = c.backward(out, lse, status=status)
+        assert status.item() == paro.PA_ERR_DEVICE_CHECK
+        assert dq[rows].isnan().all()
+        dq[rows] = 0
+        check({"dq": dq, "dk": dk, "dv": dv}, want, bounds, ("dq", "dk", "dv"))
+        first = first or (dq, dk, dv)
+        assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), first))
