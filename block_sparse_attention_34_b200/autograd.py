@@ -17,11 +17,21 @@ from torch.autograd.function import once_differentiable
 from . import paro
 
 
-def _rows(g):
-    """A gradient as the library takes it: rows contiguous and aligned."""
-    e = 16 // g.element_size()
-    fine = g.stride(3) == 1 and g.data_ptr() % 16 == 0 and all(g.stride(i) % e == 0 for i in range(3))
-    return g if fine else g.contiguous()
+def _rows(t):
+    """``t``, or a copy, as the library takes it with strides: rows contiguous,
+    each at a multiple of 16 bytes.  (A gradient lies where autograd put it: that
+    of a part of a concatenation may start anywhere, contiguous or not.)"""
+    e = 16 // t.element_size()
+    fine = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(
+        t.shape[i] == 1 or t.stride(i) % e == 0 for i in range(3))
+    return t if fine else t.clone(memory_format=torch.contiguous_format)
+
+
+def _whole(t):
+    """``t``, or a copy, as the library takes it without: contiguous from a
+    multiple of 16 bytes on."""
+    fine = t.is_contiguous() and t.data_ptr() % 16 == 0
+    return t if fine else t.clone(memory_format=torch.contiguous_format)
 
 
 class _Rope3d(torch.autograd.Function):
@@ -48,11 +58,10 @@ class _SparseAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, pr, idx, counts, density, rope, status):
         if rope is None:
-            q, k = q.contiguous(), k.contiguous()
-            qp, kp = (paro.reorder(x, pr, with_pool=idx is None) for x in (q, k))
+            qp, kp = (paro.reorder(_whole(x), pr, with_pool=idx is None) for x in (q, k))
         else:
             qp, kp = (paro.rope_reorder(_rows(x), rope, pr, with_pool=idx is None) for x in (q, k))
-        vp = paro.reorder(v.contiguous(), pr)
+        vp = paro.reorder(_whole(v), pr)
         if idx is None:
             (qp, q_pool), (kp, k_pool) = qp, kp
             idx = paro.select_topk(paro.score_pooled(q_pool, k_pool, pr), pr,
@@ -69,7 +78,7 @@ class _SparseAttention(torch.autograd.Function):
         qp, kp, vp, out, lse, idx, counts = ctx.saved_tensors
         if dout is None and dlse is None:
             return (None,) * 9
-        dout = torch.zeros_like(out) if dout is None else dout.contiguous()
+        dout = torch.zeros_like(out) if dout is None else _whole(dout)
         dlse = None if dlse is None else dlse.contiguous()
         dq, dk, dv = paro.block_sparse_attn_backward(dout, qp, kp, vp, out, lse, ctx.pr, idx, counts,
                                                      dlse=dlse, status=ctx.status)

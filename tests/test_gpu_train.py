@@ -404,3 +404,37 @@ def test_malformed_lists_among_many_blocks(block, d):
         check({"dq": dq, "dk": dk, "dv": dv}, want, bounds, ("dq", "dk", "dv"))
         first = first or (dq, dk, dv)
         assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), first))
+
+
+@pytest.mark.parametrize("rotated", [False, True])
+def test_gradients_and_inputs_that_start_anywhere(rotated):
+    """A part of a concatenation hands its gradient over at any address."""
+    pr = paro.Problem(1, 2, (3, 8, 9), 64, 64, [0, 5])
+    table = paro.RopeTable((3, 8, 9), 64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    data = [torch.randn(pr.natural, generator=g, device="cuda").to(BF) for _ in range(3)]
+    w = torch.randn(3 + data[0].numel(), generator=g, device="cuda").to(BF)
+
+    def grads(join, place):
+        leaves = [place(x).requires_grad_() for x in data]
+        out, _ = autograd.sparse_attention(*leaves, pr, density=0.5, rope=table if rotated else None)
+        x = place(data[0]).requires_grad_()
+        turned = autograd.rope3d(x, table) if x.data_ptr() % 16 == 0 else None
+        both = [t for t in (out, turned) if t is not None]
+        for t in both:
+            if join:
+                t = torch.cat((torch.zeros(3, dtype=BF, device="cuda"), t.flatten()))
+                (t * w).sum().backward()
+            else:
+                (t * w[3:].clone().view(pr.natural)).sum().backward()
+        return [x.grad for x in leaves] + ([x.grad] if turned is not None else [])
+
+    def odd(x):
+        return torch.cat((x.new_zeros(1), x.flatten()))[1:].view(x.shape)
+
+    want = grads(False, torch.clone)
+    for a, b in zip(grads(True, torch.clone), want):
+        assert torch.equal(a, b)
+    for a, b in zip(grads(True, odd), want[:3]):
+        assert torch.equal(a, b)
