@@ -13,10 +13,11 @@
 //   P = 2^(X c - lse),  dS = P o (Y - D)
 //   G1 += dS^T B1 (dK or dQ),  kKeys: G2 += P^T B2 (dV)   64 x d
 // P and dS go to shared memory as bf16, one after the other into one buffer, a
-// row a thread, and are the (M-major) A operand of the second products.  An odd list's last step holds
-// its block twice, with P = dS = 0 in the second place: nothing but the
+// row a thread, and are the (M-major) A operand of the second products.  The
+// second place of an odd list's last step is loaded from behind the tensors'
+// end, as zeros, with P = dS = 0 whatever the own block holds: nothing but the
 // block's own kept tiles meets its sums, so what other rows hold (infinities,
-// NaN) stays there.
+// NaN) stays there, and an infinity of its own meets no weight of zero.
 //
 // 10 warps:
 //   0-7  elementwise: warp w holds the streamed rows 32 (w % 4) .. +31 (a row
@@ -31,7 +32,7 @@
 //
 // Bounded by the chain X, P, Y, dS of a step; at d = 64 two CTAs share an SM
 // and fill each other's gaps.  Measured, d = 64: 307200 tiles in each use
-// 1.95 ms (mma.sync, which takes 4 times the tensor pipe's cycles: 4.72 ms;
+// 1.94 ms (mma.sync, which takes 4 times the tensor pipe's cycles: 4.72 ms;
 // two load warps, which leave 80 registers: 2.00; with a buffer each for P and
 // dS and so only two stages of B1 2.23); 1280 tiles of 128 + 128 lists 21.3 us
 // (29.4); the same at d = 128 30.9 us (51), where one CTA fits an SM.
@@ -133,12 +134,14 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
         return __shfl_sync(0xffffffffu, id_lane, e & 31);
       }
     };
+    const int end = (int)gridDim.y * g.Np;  // rows behind it read as zero
     auto load = [&](const CUtensorMap* map, uint32_t to, int j0, int j1, uint32_t b) {
       mbar_arrive_tx(b, L::kTile);  // release: the ids are visible behind the barrier
+      const int y0 = head + j0 * kBlock, y1 = j1 < 0 ? end : head + j1 * kBlock;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
-        tma_load_2d(to + h * kHalf, map, 64 * h, head + j0 * kBlock, b);
-        tma_load_2d(to + h * kHalf + kOwnHalf, map, 64 * h, head + j1 * kBlock, b);
+        tma_load_2d(to + h * kHalf, map, 64 * h, y0, b);
+        tma_load_2d(to + h * kHalf + kOwnHalf, map, 64 * h, y1, b);
       }
     };
     auto g1_done = [&](int t) {
@@ -148,11 +151,11 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
     for (int t = 0; t < n; ++t) {
       const int s1 = t % kB1Stages, s2 = t & 1;
       const bool two = 2 * t + 1 < cnt;
-      const int j0 = entry(2 * t), j1 = two ? entry(2 * t + 1) : j0;
+      const int j0 = entry(2 * t), j1 = two ? entry(2 * t + 1) : -1;
       if (!g1_done(t - kB1Stages)) break;
       if (lane == 0) {
         step_ids[2 * s1] = j0;
-        step_ids[2 * s1 + 1] = two ? j1 : -1;
+        step_ids[2 * s1 + 1] = j1;
         load(&map_b1, base + L::kB1 + s1 * L::kTile, j0, j1, bar(BB1 + s1));
       }
       issued1 = t + 1;
@@ -283,12 +286,13 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
       }
       if constexpr (kKeys) {
         if (t > 0 && !(ok = warp_wait(bar(BG1 + (t - 1) % kB1Stages), ((t - 1) / kB1Stages) & 1, ctl))) break;
+        // (0 where there is no row: 0 times an infinite key is NaN)
+        auto pair = [&](float2 f) { return was_valid ? pack_bf16(f.x, f.y) : 0u; };
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2* f = p + 4 * c;
           p_row[(4 * half + c) ^ (r & 7)] =
-              make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y),
-                         pack_bf16(f[2].x, f[2].y), pack_bf16(f[3].x, f[3].y));
+              make_uint4(pair(f[0]), pair(f[1]), pair(f[2]), pair(f[3]));
         }
       }
       if constexpr (kKeys) fence_async_smem();
@@ -314,7 +318,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& map_a1, const CUten
             fadd2(make_float2(__uint_as_float(x[2 * c + 2]), __uint_as_float(x[2 * c + 3])), n1));
         pk[c] = pack_bf16(s0.x, s0.y);
         pk[c + 1] = pack_bf16(s1.x, s1.y);
-        if (!kKeys && !was_valid) pk[c] = pk[c + 1] = 0u;  // (kKeys: P is 0 there)
+        if (!was_valid) pk[c] = pk[c + 1] = 0u;
       }
       // the buffer is free once the product of P(t), or of dS(t - 1), is done
       if (kKeys ? !(ok = warp_wait(bar(BG2 + (t & 1)), (t >> 1) & 1, ctl))

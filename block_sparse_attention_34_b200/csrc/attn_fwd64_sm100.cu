@@ -166,12 +166,14 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
         tma_load_2d(base + L::kQ + h * kOwnHalf, &map_q, 64 * h, head + blk * kBlock, bar(BQ));
     }
     int issued_k = 0, issued_v = 0, id_lane = 0;  // id_lane: entry 32 (e / 32) + lane
+    const int end = (int)gridDim.y * g.Np;  // rows behind it read as zero
     auto load = [&](const CUtensorMap* map, uint32_t to, int j0, int j1, uint32_t b) {
       mbar_arrive_tx(b, L::kTile);  // release: the ids are visible behind the barrier
+      const int y0 = head + j0 * kBlock, y1 = j1 < 0 ? end : head + j1 * kBlock;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
-        tma_load_2d(to + h * kHalf, map, 64 * h, head + j0 * kBlock, b);
-        tma_load_2d(to + h * kHalf + kOwnHalf, map, 64 * h, head + (j1 < 0 ? j0 : j1) * kBlock, b);
+        tma_load_2d(to + h * kHalf, map, 64 * h, y0, b);
+        tma_load_2d(to + h * kHalf + kOwnHalf, map, 64 * h, y1, b);
       }
     };
     // the step that had a stage is over: nothing of it is read any more
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
       if (!over(t - kKStages)) break;
       if (lane == 0) {
         step_ids[2 * sk] = j0;
-        step_ids[2 * sk + 1] = j1;  // -1: an odd list's end, which holds its block twice
+        step_ids[2 * sk + 1] = j1;  // -1: an odd list's end, whose second place is zero
         load(&map_k, base + L::kK + sk * L::kTile, j0, j1, bar(BK + sk));
       }
       issued_k = t + 1;

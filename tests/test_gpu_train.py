@@ -438,3 +438,32 @@ def test_gradients_and_inputs_that_start_anywhere(rotated):
         assert torch.equal(a, b)
     for a, b in zip(grads(True, odd), want[:3]):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("k", [1, 2, 3])
+@pytest.mark.parametrize("block,d", [(64, 64), (64, 128), (128, 64), (128, 128)])
+def test_an_infinity_stays_one(block, d, k):
+    """An infinite value or gradient gives infinities where its weight meets
+    it, for lists of odd and of even length, and touches nothing else."""
+    c = Case(1, 2, d, block, (4, 13, 16), (0, 0), k, seed=k)  # order FHW: positions are tokens
+    out, lse = c.forward()
+    grads = c.backward(out, lse)
+    keep = torch.zeros(c.pr.square, dtype=torch.bool, device="cuda").scatter_(3, c.idx.long(), True)
+    of = torch.arange(c.pr.N, device="cuda") // block
+    j = int(c.idx[0, 0, 1, -1])  # kept by the second block of the first head
+    at = min(j * block + 9, c.pr.N - 1)
+
+    clean = c.perm[2].clone()
+    c.perm[2][0, 0, at, 5] = float("inf")
+    got, same = c.forward()
+    assert torch.equal(same, lse)
+    want = out.clone()
+    want[0, 0, :, 5] = torch.where(keep[0, 0, of, j], float("inf"), want[0, 0, :, 5].float()).to(BF)
+    assert torch.equal(got, want)
+
+    c.perm[2], at = clean, block + 3
+    c.do[0, 0, at, 7] = float("inf")
+    dv = c.backward(out, lse)[2]
+    want = grads[2].clone()
+    want[0, 0, :, 7] = torch.where(keep[0, 0, 1, of], float("inf"), want[0, 0, :, 7].float()).to(BF)
+    assert torch.equal(dv, want)
