@@ -204,6 +204,15 @@ class Problem:
         self.square = (self.B, self.heads, self.NB, self.NB)
         self.per_block = (self.B, self.heads, self.NB)
 
+    # a copy or a pickle carries the order ids, and points to its own
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "perms_ptr"}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._perms = np.ascontiguousarray(self._perms)
+        self.perms_ptr = self._perms.ctypes.data_as(ctypes.c_void_p)
+
     @classmethod
     def from_qkv(cls, q, grid, perms, block):
         B, h, N, d = q.shape

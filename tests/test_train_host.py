@@ -2,8 +2,10 @@
 queries: what the library and the binding refuse before any launch (so these
 run without a GPU)."""
 
+import copy
 import ctypes
 import os
+import pickle
 
 import numpy as np
 import pytest
@@ -205,3 +207,30 @@ def test_the_binding_checks_every_tensor(lib, device_blind):
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"case {i} was accepted")
+
+
+def test_a_problem_is_copied_and_pickled(lib):
+    """Copies stand alone: their pointer is to their own order ids."""
+    pr = paro.Problem(1, 3, (3, 8, 9), 64, 64, [0, 5, 9])
+    paro.backward_workspace(pr)
+    for other in (copy.copy(pr), copy.deepcopy(pr), pickle.loads(pickle.dumps(pr)),
+                  copy.deepcopy({"problem": pr})["problem"]):
+        assert other.perms_ptr.value == other._perms.ctypes.data
+        assert list(ctypes.cast(other.perms_ptr, ctypes.POINTER(ctypes.c_int8))[:3]) == [0, 5, 9]
+        assert bytes(other.shape) == bytes(pr.shape)
+        for name in ("B", "heads", "N", "NB", "N_p", "workspace", "natural", "rows", "permuted", "pooled",
+                     "square", "per_block"):
+            assert getattr(other, name) == getattr(pr, name)
+    del pr
+    assert list(ctypes.cast(other.perms_ptr, ctypes.POINTER(ctypes.c_int8))[:3]) == [0, 5, 9]
+
+
+def test_a_module_that_holds_one_is_copied(lib):
+    class Layer(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.w = torch.nn.Parameter(torch.zeros(3))
+            self.problem = paro.Problem(1, 2, (4, 8, 8), 64, 64, [1, 7])
+
+    ema = copy.deepcopy(Layer())
+    assert list(ctypes.cast(ema.problem.perms_ptr, ctypes.POINTER(ctypes.c_int8))[:2]) == [1, 7]
