@@ -1,9 +1,9 @@
 """Thin Python binding of libparo (include/paro.h).
 
 Argument marshalling only: every step runs in the library's CUDA kernels on
-the caller's current torch stream.  Torch supplies device memory and
-streams.  There is no CPU fallback: if the library is missing or a call
-fails, an exception is raised.
+the current torch stream of its tensors' device, whichever device is current.
+Torch supplies device memory and streams.  There is no CPU fallback: if the
+library is missing or a call fails, an exception is raised.
 """
 
 from __future__ import annotations
@@ -123,12 +123,30 @@ def _check(status: int):
         raise ParoError(status, load().pa_last_error().decode())
 
 
-def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The current stream of the current device."""
+    return _raw_stream(_current_device())
+
+
+def _launch(t, fn, *args):
+    """fn(*args, stream) on the device of ``t`` and that device's current
+    stream, as torch's own operators run: the one way every entry launches, so
+    that the steps of a call stay in order whichever device is current."""
+    i = t.get_device()
+    if i < 0 or i == _current_device():  # (host tensors end at every entry's checks)
+        status = fn(*args, _stream())
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, _stream())
+    _check(status)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -223,7 +241,7 @@ def clear_status(status):
     """Enqueue status[0] = PA_OK on the current stream (a memset)."""
     _need_cuda(status)
     _expect_status(status)
-    _check(load().pa_clear_status(_ptr(status), _stream()))
+    _launch(status, load().pa_clear_status, _addr(status))
 
 
 def test_inject_v_stall(query_block: int, batch_head: int, tile: int, wait_limit_ns: int):
@@ -261,8 +279,7 @@ def inverse_reorder(xp, pr: Problem, out=None):
     _expect(out, "out", pr.natural, xp.dtype)
     out = out if out is not None else torch.empty((pr.B, pr.heads, pr.N, pr.d), dtype=xp.dtype,
                                                   device=xp.device)
-    _check(load().pa_inverse_reorder(_ptr(xp), _ptr(out), _dtype_code(xp), pr.shape, pr.perms_ptr,
-                                     _stream()))
+    _launch(xp, load().pa_inverse_reorder, _addr(xp), _addr(out), _dtype_code(xp), pr.shape, pr.perms_ptr)
     return out
 
 
@@ -277,8 +294,8 @@ def block_score(q, k, pr: Problem, q_pool=None, k_pool=None, scores=None):
     q_pool = q_pool if q_pool is not None else torch.empty((pr.B, pr.heads, pr.NB, pr.d), dtype=torch.float32, device=dev)
     k_pool = k_pool if k_pool is not None else torch.empty_like(q_pool)
     scores = scores if scores is not None else torch.empty((pr.B, pr.heads, pr.NB, pr.NB), dtype=torch.float32, device=dev)
-    _check(load().pa_block_score(_ptr(q), _ptr(k), _dtype_code(q), pr.shape, pr.perms_ptr,
-                                 _ptr(q_pool), _ptr(k_pool), _ptr(scores), _stream()))
+    _launch(q, load().pa_block_score, _addr(q), _addr(k), _dtype_code(q), pr.shape, pr.perms_ptr,
+            _addr(q_pool), _addr(k_pool), _addr(scores))
     return q_pool, k_pool, scores
 
 
@@ -288,7 +305,7 @@ def score_pooled(q_pool, k_pool, pr: Problem, scores=None):
     _expect(k_pool, "k_pool", pr.pooled, torch.float32)
     _expect(scores, "scores", pr.square, torch.float32)
     scores = scores if scores is not None else torch.empty((pr.B, pr.heads, pr.NB, pr.NB), dtype=torch.float32, device=q_pool.device)
-    _check(load().pa_score_pooled(_ptr(q_pool), _ptr(k_pool), pr.shape, _ptr(scores), _stream()))
+    _launch(q_pool, load().pa_score_pooled, _addr(q_pool), _addr(k_pool), pr.shape, _addr(scores))
     return scores
 
 
@@ -297,7 +314,7 @@ def select_topk(scores, pr: Problem, k: int, idx=None):
     _expect(scores, "scores", pr.square, torch.float32)
     _expect(idx, "idx", pr.per_block + (int(k),), torch.int32)
     idx = idx if idx is not None else torch.empty((pr.B, pr.heads, pr.NB, k), dtype=torch.int32, device=scores.device)
-    _check(load().pa_select_topk(_ptr(scores), pr.shape, int(k), _ptr(idx), _stream()))
+    _launch(scores, load().pa_select_topk, _addr(scores), pr.shape, int(k), _addr(idx))
     return idx
 
 
@@ -309,7 +326,7 @@ def compact_mask(bitmask, pr: Problem, idx=None, counts=None):
     dev = bitmask.device
     idx = idx if idx is not None else torch.empty((pr.B, pr.heads, pr.NB, pr.NB), dtype=torch.int32, device=dev)
     counts = counts if counts is not None else torch.empty((pr.B, pr.heads, pr.NB), dtype=torch.int32, device=dev)
-    _check(load().pa_compact_mask(_ptr(bitmask), pr.shape, _ptr(idx), _ptr(counts), _stream()))
+    _launch(bitmask, load().pa_compact_mask, _addr(bitmask), pr.shape, _addr(idx), _addr(counts))
     return idx, counts
 
 
@@ -323,8 +340,8 @@ def select_hybrid(scores, pr: Problem, k: int, top_p: float, window: int, idx=No
     dev = scores.device
     idx = idx if idx is not None else torch.empty((pr.B, pr.heads, pr.NB, pr.NB), dtype=torch.int32, device=dev)
     counts = counts if counts is not None else torch.empty((pr.B, pr.heads, pr.NB), dtype=torch.int32, device=dev)
-    _check(load().pa_select_hybrid(_ptr(scores), pr.shape, int(k), float(top_p), int(window), _ptr(idx),
-                                   _ptr(counts), _stream()))
+    _launch(scores, load().pa_select_hybrid, _addr(scores), pr.shape, int(k), float(top_p), int(window),
+            _addr(idx), _addr(counts))
     return idx, counts
 
 
@@ -340,22 +357,23 @@ def sics_scores(q, k, pr: Problem, scores=None, orders=None):
     _expect(orders, "orders", (pr.heads,), torch.int8)
     scores = scores if scores is not None else torch.empty((pr.B, pr.heads, N_ORDERS), dtype=torch.float32, device=q.device)
     orders = orders if orders is not None else torch.empty((pr.heads,), dtype=torch.int8, device=q.device)
-    _check(load().pa_sics_scores(_ptr(q), _ptr(k), _dtype_code(q), pr.shape, _ptr(scores),
-                                 _ptr(orders), _stream()))
+    _launch(q, load().pa_sics_scores, _addr(q), _addr(k), _dtype_code(q), pr.shape, _addr(scores),
+            _addr(orders))
     return scores, orders
 
 
 def map_row_stats(q_perm, k_perm, pr: Problem, order: int, status=None):
     """Row softmax (log2 max, sum) of every token of the dense map, from
     copies of q, k permuted by ``order`` -> ([B,h,N], [B,h,N])."""
-    _need_cuda(q_perm, k_perm)
+    _need_cuda(q_perm, k_perm, status)
+    _expect_status(status)
     _expect(q_perm, "q_perm", pr.permuted, torch.bfloat16)
     _expect(k_perm, "k_perm", pr.permuted, torch.bfloat16)
     dev = q_perm.device
     m = torch.empty((pr.B, pr.heads, pr.N), dtype=torch.float32, device=dev)
     l = torch.empty_like(m)
-    _check(load().pa_map_row_stats(_ptr(q_perm), _ptr(k_perm), pr.shape, int(order), _ptr(m),
-                                   _ptr(l), _ptr(status), _stream()))
+    _launch(q_perm, load().pa_map_row_stats, _addr(q_perm), _addr(k_perm), pr.shape, int(order), _addr(m),
+            _addr(l), _addr(status))
     return m, l
 
 
@@ -363,7 +381,8 @@ def map_block_stats(q_perm, k_perm, pr: Problem, order: int, row_max, row_sum, e
                     with_log=True, status=None):
     """Per block of the map in ``order``: dict of [B,h,NB,NB] count / total
     / peak (and log_total)."""
-    _need_cuda(q_perm, k_perm, row_max, row_sum)
+    _need_cuda(q_perm, k_perm, row_max, row_sum, status)
+    _expect_status(status)
     _expect(q_perm, "q_perm", pr.permuted, torch.bfloat16)
     _expect(k_perm, "k_perm", pr.permuted, torch.bfloat16)
     _expect(row_max, "row_max", (pr.B, pr.heads, pr.N), torch.float32)
@@ -372,10 +391,9 @@ def map_block_stats(q_perm, k_perm, pr: Problem, order: int, row_max, row_sum, e
     out = {key: torch.empty((pr.B, pr.heads, pr.NB, pr.NB), dtype=torch.float32, device=dev)
            for key in ("count", "total", "peak")}
     out["log_total"] = torch.empty_like(out["total"]) if with_log else None
-    _check(load().pa_map_block_stats(_ptr(q_perm), _ptr(k_perm), pr.shape, int(order),
-                                     _ptr(row_max), _ptr(row_sum), float(eps), _ptr(out["count"]),
-                                     _ptr(out["total"]), _ptr(out["peak"]),
-                                     _ptr(out["log_total"]), _ptr(status), _stream()))
+    _launch(q_perm, load().pa_map_block_stats, _addr(q_perm), _addr(k_perm), pr.shape, int(order),
+            _addr(row_max), _addr(row_sum), float(eps), _addr(out["count"]), _addr(out["total"]),
+            _addr(out["peak"]), _addr(out["log_total"]), _addr(status))
     return out
 
 
@@ -400,14 +418,14 @@ def paro_offline(q, k, grid, block, eps=1e-3, rho=0.9, alpha=0.5, sigma=0.9, sta
         if row_max is None:
             row_max, row_sum = map_row_stats(qp, kp, pr, o, status)
         st = map_block_stats(qp, kp, pr, o, row_max, row_sum, eps, True, status)
-        _check(load().pa_paro_metric(_ptr(st["count"]), _ptr(st["total"]), _ptr(st["peak"]),
-                                     pr.shape, o, float(rho), _ptr(sf), _ptr(inc), _stream()))
+        _launch(sf, load().pa_paro_metric, _addr(st["count"]), _addr(st["total"]), _addr(st["peak"]),
+                pr.shape, o, float(rho), _addr(sf), _addr(inc))
         select_hybrid(st["log_total"], pr, 0, sigma, -1, idx_all[o], cnt_all[o])
         del qp, kp, st
     metric = torch.empty_like(sf)
     orders = torch.empty((B, heads), dtype=torch.int8, device=dev)
-    _check(load().pa_paro_choose(_ptr(sf), _ptr(inc), pr0.shape, float(alpha), _ptr(metric),
-                                 _ptr(orders), _stream()))
+    _launch(sf, load().pa_paro_choose, _addr(sf), _addr(inc), pr0.shape, float(alpha), _addr(metric),
+            _addr(orders))
     # each head's mask in its chosen order (a gather of the six candidates)
     pick = orders.long()
     bi = torch.arange(B, device=dev)[:, None]
@@ -432,8 +450,8 @@ def quantize_int8(x, pr: Problem, with_pool=False, x_q=None, scales=None, pool=N
     if bits not in (4, 8):
         raise ValueError(f"bits={bits}: 4 or 8")
     fn = load().pa_quantize_int8 if bits == 8 else load().pa_quantize_int4
-    _check(fn(_ptr(x), _dtype_code(x), pr.shape, pr.perms_ptr, _ptr(x_q),
-                                   _ptr(scales), _ptr(pool), _stream()))
+    _launch(x, fn, _addr(x), _dtype_code(x), pr.shape, pr.perms_ptr, _addr(x_q), _addr(scales),
+            _addr(pool))
     return (x_q, scales, pool) if with_pool else (x_q, scales)
 
 
@@ -482,17 +500,14 @@ def block_sparse_attn(q, k, v, pr: Problem, idx, counts=None, scales=None, out=N
     k_max = int(idx.shape[-1])
     flags = ((PA_ATTN_PERMUTED if permuted else 0) | (PA_ATTN_P4 if p4 else 0)
              | (PA_ATTN_P_TILE if p_tile else 0))
-    lib = load()
     if baseline:
-        st = lib.pa_block_sparse_attn_mma(_ptr(q), _ptr(k), _ptr(v), code, flags, pr.shape,
-                                          pr.perms_ptr, _ptr(idx), _ptr(counts), k_max, _ptr(out),
-                                          _ptr(status), _stream())
+        _launch(q, load().pa_block_sparse_attn_mma, _addr(q), _addr(k), _addr(v), code, flags,
+                pr.shape, pr.perms_ptr, _addr(idx), _addr(counts), k_max, _addr(out), _addr(status))
     else:
         qs, ks, vs = scales if scales is not None else (None, None, None)
-        st = lib.pa_block_sparse_attn(_ptr(q), _ptr(k), _ptr(v), code, flags, pr.shape,
-                                      pr.perms_ptr, _ptr(idx), _ptr(counts), k_max, _ptr(qs),
-                                      _ptr(ks), _ptr(vs), _ptr(out), _ptr(status), _stream())
-    _check(st)
+        _launch(q, load().pa_block_sparse_attn, _addr(q), _addr(k), _addr(v), code, flags, pr.shape,
+                pr.perms_ptr, _addr(idx), _addr(counts), k_max, _addr(qs), _addr(ks), _addr(vs),
+                _addr(out), _addr(status))
     return out
 
 
@@ -520,11 +535,10 @@ def block_sparse_attn_compensated(q, k, v, pr: Problem, idx, k_pool, v_pool, cou
     _expect_status(status)
     out = out if out is not None else torch.empty((pr.B, pr.heads, pr.N, pr.d), dtype=q.dtype,
                                                   device=q.device)
-    st = load().pa_block_sparse_attn_compensated(
-        _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), PA_ATTN_PERMUTED if permuted else 0, pr.shape,
-        pr.perms_ptr, _ptr(idx), _ptr(counts), int(idx.shape[-1]), _ptr(k_pool), _ptr(v_pool),
-        _dtype_code(k_pool), _ptr(out), _ptr(status), _stream())
-    _check(st)
+    _launch(q, load().pa_block_sparse_attn_compensated, _addr(q), _addr(k), _addr(v),
+            _dtype_code(q), PA_ATTN_PERMUTED if permuted else 0, pr.shape, pr.perms_ptr, _addr(idx),
+            _addr(counts), int(idx.shape[-1]), _addr(k_pool), _addr(v_pool), _dtype_code(k_pool),
+            _addr(out), _addr(status))
     return out
 
 
@@ -539,24 +553,8 @@ def round_bf16(x, out=None):
         out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
     elif out.dtype != torch.bfloat16 or out.shape != x.shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bfloat16 tensor of shape {tuple(x.shape)}")
-    _check(load().pa_round_bf16(_ptr(x), _ptr(out), x.numel(), _stream()))
+    _launch(x, load().pa_round_bf16, _addr(x), _addr(out), x.numel())
     return out
-
-
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _launch(t, fn, *args):
-    """fn(*args, stream) on the device of ``t`` and its current stream."""
-    i = t.get_device()
-    if i == _current_device():
-        status = fn(*args, _raw_stream(i))
-    else:
-        with torch.cuda.device(i):
-            status = fn(*args, _raw_stream(i))
-    if status != PA_OK:
-        raise ParoError(status, load().pa_last_error().decode())
 
 
 def _device_of(t):
@@ -592,10 +590,6 @@ def _need_lists(i, idx, counts, pr):
     _need(i, "idx", idx, pr.per_block + (idx.shape[3],), torch.int32)
     if counts is not None:
         _need(i, "counts", counts, pr.per_block, torch.int32)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 @functools.lru_cache(maxsize=256)
