@@ -36,22 +36,22 @@ def _whole(t):
 
 class _Rope3d(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, rope, positions, inverse, status):
-        ctx.rope, ctx.inverse, ctx.status = rope, inverse, status
+    def forward(ctx, x, rope, positions, inverse, status, grid):
+        ctx.rope, ctx.inverse, ctx.status, ctx.grid = rope, inverse, status, grid
         ctx.save_for_backward(positions)
-        return paro.rope3d(x, rope, positions=positions, inverse=inverse, status=status)
+        return paro.rope3d(x, rope, positions=positions, inverse=inverse, status=status, grid=grid)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g):
         (positions,) = ctx.saved_tensors
         return paro.rope3d(_rows(g), ctx.rope, positions=positions, inverse=not ctx.inverse,
-                           status=ctx.status), None, None, None, None
+                           status=ctx.status, grid=ctx.grid), None, None, None, None, None
 
 
-def rope3d(x, rope, positions=None, inverse=False, status=None):
+def rope3d(x, rope, positions=None, inverse=False, status=None, grid=None):
     """:func:`paro.rope3d`, differentiable in x."""
-    return _Rope3d.apply(x, rope, positions, inverse, status)
+    return _Rope3d.apply(x, rope, positions, inverse, status, grid)
 
 
 class _SparseAttention(torch.autograd.Function):

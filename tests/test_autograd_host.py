@@ -106,3 +106,11 @@ def test_what_fits_is_not_copied():
     assert autograd._rows(one) is one  # the stride of one element says nothing
     for t in (odd((2, 3, 8, 64)), torch.zeros(2, 3, 8, 66, dtype=BF)[..., :64], x[..., ::2]):
         assert fine(autograd._rows(t)) and torch.equal(autograd._rows(t), t)
+
+
+def test_a_table_larger_than_the_clip(calls):
+    """``grid`` places the tokens, forward and back, as in paro.rope3d."""
+    x = torch.randn(1, 2, 24, 64).requires_grad_()
+    autograd.rope3d(x, None, grid=(2, 3, 4)).sum().backward()
+    assert [(name, kw["grid"], kw["inverse"]) for name, kw in calls] == [
+        ("rope3d", (2, 3, 4), False), ("rope3d", (2, 3, 4), True)]

@@ -201,3 +201,22 @@ def test_attention_and_pipeline_rotate_first(kw):
         pipe = Pipeline(1, heads, grid, d, 128, [0, 4, 8], 1.0, rope=table, **kw)
         assert torch.equal(pipe.run(q, k, v), want)
         assert torch.equal(pipe.run(q, k, v), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_differentiable_on_a_table_larger_than_the_clip(dtype):
+    """grid=, and the gradient against the formula's and along a direction."""
+    d, grid = 128, (3, 4, 6)
+    table = paro.RopeTable((5, 9, 7), d)
+    x, w = random((2, 3, 72, d), dtype, 1).requires_grad_(), random((2, 3, 72, d), dtype, 2)
+    y = autograd.rope3d(x, table, grid=grid)
+    assert torch.equal(y, paro.rope3d(x.detach(), table, grid=grid))
+    (g,) = torch.autograd.grad(y, x, w)
+    angles = tr.rope_angles(tr.grid_positions(grid), d, table.pairs, 10000.0)
+    check(g, w, angles, True, inverse=True)
+    v = np.random.default_rng(3).standard_normal(x.shape)  # the rotation is linear
+    diff = (tr.rope(v, angles, True) * f64(w)).sum()
+    bound = tr.rope_bounds(f64(w), tr.rope(f64(w), angles, True, True), True, dtype == BF)
+    assert abs(diff - (f64(g) * v).sum()) <= (bound * np.abs(v)).sum()
+    with pytest.raises(ValueError, match="grid"):
+        autograd.rope3d(x, table)
