@@ -82,11 +82,14 @@ class _SparseAttention(torch.autograd.Function):
         dlse = None if dlse is None else dlse.contiguous()
         dq, dk, dv = paro.block_sparse_attn_backward(dout, qp, kp, vp, out, lse, ctx.pr, idx, counts,
                                                      dlse=dlse, status=ctx.status)
+        # (one call computes the three: what nobody asked for goes no further)
+        grads = [g if need else None for g, need in zip((dq, dk, dv), ctx.needs_input_grad)]
         if ctx.rope is not None:
             grid = (ctx.pr.F, ctx.pr.H, ctx.pr.W)
-            for g in (dq, dk):
-                paro.rope3d(g, ctx.rope, grid=grid, inverse=True, out=g)
-        return dq, dk, dv, None, None, None, None, None, None
+            for g in grads[:2]:
+                if g is not None:
+                    paro.rope3d(g, ctx.rope, grid=grid, inverse=True, out=g)
+        return (*grads, None, None, None, None, None, None)
 
 
 def sparse_attention(q, k, v, pr, idx=None, counts=None, density=None, rope=None, status=None):

@@ -114,3 +114,13 @@ def test_a_table_larger_than_the_clip(calls):
     autograd.rope3d(x, None, grid=(2, 3, 4)).sum().backward()
     assert [(name, kw["grid"], kw["inverse"]) for name, kw in calls] == [
         ("rope3d", (2, 3, 4), False), ("rope3d", (2, 3, 4), True)]
+
+
+@pytest.mark.parametrize("need", [(True, False, False), (False, True, True), (False, False, True), (True, True, True)])
+def test_only_the_gradients_asked_for(calls, problem, need):
+    """What nobody asked for is neither turned back nor handed on."""
+    leaves = [torch.randn(problem.natural).to(BF).requires_grad_(n) for n in need]
+    out, _ = autograd.sparse_attention(*leaves, problem, density=0.5, rope="table")
+    out.sum().backward()
+    assert [x.grad is not None for x in leaves] == list(need)
+    assert [name for name, _ in calls] == ["backward"] + ["rope3d"] * sum(need[:2])
