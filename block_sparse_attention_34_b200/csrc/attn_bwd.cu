@@ -15,10 +15,10 @@
 // through L2 would cost about as much as the two products).
 //
 // Preparation: dO is copied to the permuted order with each row's -lse (log2
-// units) and -D beside it, pad rows as (-inf, 0) so that they drop out of
-// every sum as P = 0; the kept lists are transposed to one bit per (key
-// block, query block).  One launch, and one for both gradient kernels: a
-// small call is bound by its launches.
+// units) and -D beside it, pad rows and rows whose log-sum-exp is -inf with
+// -inf, so that they drop out of every sum as P = 0; the kept lists are
+// transposed to one bit per (key block, query block).  One launch, and one for
+// both gradient kernels: a small call is bound by its launches.
 #include "bwd.cuh"
 
 namespace paro {
@@ -101,7 +101,9 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t prow = bh * g.Np + p;
   reinterpret_cast<uint4*>(dop + prow * D)[c] = d;
   if (c == 0) {
-    nlse[prow] = row >= 0 ? -__ldg(lse + row) * kLog2e : -INFINITY;
+    // a row whose keys all scored -inf has no weights either
+    const float x = row >= 0 ? __ldg(lse + row) : -INFINITY;
+    nlse[prow] = x == -INFINITY ? -INFINITY : -x * kLog2e;
     ndel[prow] = row >= 0 ? (dlse != nullptr ? __ldg(dlse + row) : 0.f) - s : 0.f;
   }
 }

@@ -498,7 +498,8 @@ PA_API int64_t pa_block_sparse_attn_backward_workspace(pa_shape shape);
  * [B,heads,N] float.  idx, counts, k_max as in the forward pass; the
  * selection itself is not differentiated.  P and dS are rounded to bf16 for
  * their products; every sum is fp32, in the same order on every run.  Rows
- * without kept blocks get dq = 0, keys that no row keeps dk = dv = 0.  A
+ * without kept blocks, or whose scores are all -inf (lse -inf), get dq = 0 and
+ * add nothing to dk and dv; keys that no row keeps get dk = dv = 0.  A
  * malformed list is reported on dev_status (PA_ERR_DEVICE_CHECK): its rows
  * of dq are left unwritten and it adds nothing to dk and dv.
  * workspace: pa_block_sparse_attn_backward_workspace bytes, device memory,

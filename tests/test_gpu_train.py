@@ -467,3 +467,33 @@ def test_an_infinity_stays_one(block, d, k):
     want = grads[2].clone()
     want[0, 0, :, 7] = torch.where(keep[0, 0, 1, of], float("inf"), want[0, 0, :, 7].float()).to(BF)
     assert torch.equal(dv, want)
+
+
+@pytest.mark.parametrize("block,d", [(128, 128), (128, 64), (64, 128), (64, 64)])
+def test_a_row_whose_keys_all_score_minus_infinity(block, d):
+    """It is a row without keys: zeros and -inf, no gradient of its own, and
+    nothing of it in its keys' gradients."""
+    c = Case(1, 1, d, block, (4, 13, 16), (0,), 3, counts="random", seed=4)  # positions are tokens
+    c.counts_np[...] = 3
+    c.counts = torch.from_numpy(c.counts_np).cuda()
+    at = [5, block + 7, c.pr.N - 1]
+    c.q[..., 0] = 0
+    c.k[..., 0] = -1e20
+    c.do[0, 0, at] = 0
+
+    def run(value):
+        c.q[0, 0, at, 0] = value
+        c.perm[:2] = [paro.reorder(x, c.pr) for x in (c.q, c.k)]
+        out, lse = c.forward()
+        return out, lse, c.backward(out, lse)
+
+    out0, lse0, want = run(0.0)
+    out, lse, _ = run(1e20)  # 1e20 * -1e20 is beyond 32 bits
+    assert (out[0, 0, at] == 0).all() and (lse[0, 0, at] == -float("inf")).all()
+    rest = torch.ones(c.pr.N, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert torch.equal(out[0, 0, rest], out0[0, 0, rest]) and torch.equal(lse[0, 0, rest], lse0[0, 0, rest])
+    c.do[0, 0, at] = 3.0
+    dq, dk, dv = c.backward(out, lse)
+    assert (dq[0, 0, at] == 0).all() and torch.equal(dq[0, 0, rest], want[0][0, 0, rest])
+    assert torch.equal(dk, want[1]) and torch.equal(dv, want[2])
