@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int64_t nat =
           mine ? bh * g.N + natural_index(g, g.perm[(int)(bh % g.heads)], pos) : 0;
-      if (mine && half == 0) lse[nat] = sum == 0.f ? -INFINITY : row_lse(-neg_ref[row], sum);
+      if (mine && half == 0) lse[nat] = row_lse(-neg_ref[row], sum);
       uint4* to = reinterpret_cast<uint4*>(out + nat * D);
 #pragma unroll
       for (int c = 0; c < D / 2; c += 32) {

@@ -696,7 +696,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lt = (m0 == -INFINITY ? 0.f : lsum[r] * ex2(m0 - m)) +
                          (m1 == -INFINITY ? 0.f : lsum[128 + r] * ex2(m1 - m));
         inv = lt > 0.f ? 1.f / lt : 0.f;
-        if (kLse && nat >= 0 && grp == 0) lse[nat] = row_lse(m, lt);
+        // (a NaN sum counts even where its group's reference is -inf)
+        if (kLse && nat >= 0 && grp == 0)
+          lse[nat] = row_lse(m, lt + 0.f * (lsum[r] + lsum[128 + r]));
       }
       // every P V has completed once the last one's commit fired
       if (okm) okm = warp_wait(pv_done(n_tiles - 1), ring_par(n_tiles - 1), ctl);

@@ -96,10 +96,10 @@ __device__ __forceinline__ int natural_index(const Grid& g, int order, int p) {
   return (a * tf + f1) * HW + (b * th + h1) * g.W + c * tw + w1;
 }
 
-// Log-sum-exp of a row from its maximum m (log2 units) and its sum l of
-// 2^(s - m); -inf for a row without keys.
+// Log-sum-exp of a row from its reference m (log2 units) and its sum l of
+// 2^(s - m): -inf for a row without weights (l = 0), NaN where a score is.
 __device__ __forceinline__ float row_lse(float m, float l) {
-  return m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // First error wins; never traps.

@@ -497,3 +497,24 @@ def test_a_row_whose_keys_all_score_minus_infinity(block, d):
     dq, dk, dv = c.backward(out, lse)
     assert (dq[0, 0, at] == 0).all() and torch.equal(dq[0, 0, rest], want[0][0, 0, rest])
     assert torch.equal(dk, want[1]) and torch.equal(dv, want[2])
+
+
+@pytest.mark.parametrize("k", [1, 2, 3])
+@pytest.mark.parametrize("block,d", [(128, 128), (128, 64), (64, 128), (64, 64)])
+def test_nan_keys_give_a_nan_log_sum(block, d, k):
+    """Where out is NaN so is lse, a block of nothing but NaN included: -inf
+    would say that the row has no keys."""
+    c = Case(1, 1, d, block, (4, 13, 16), (0,), k, seed=k)  # order FHW: positions are tokens
+    clean = c.forward()
+    keep = torch.zeros(c.pr.square, dtype=torch.bool, device="cuda").scatter_(3, c.idx.long(), True)
+    of = torch.arange(c.pr.N, device="cuda") // block
+    j = int(c.idx[0, 0, 1, 0])
+    hit = keep[0, 0, of, j]
+    for rows in (slice(0, block), slice(3, 4)):  # every key of the block, one of them
+        kp = c.perm[1].clone()
+        c.perm[1][0, 0, j * block:(j + 1) * block][rows] = float("nan")
+        out, lse = c.forward()
+        c.perm[1] = kp
+        assert out[0, 0, hit].isnan().all() and lse[0, 0, hit].isnan().all()
+        assert torch.equal(out[0, 0, ~hit], clean[0][0, 0, ~hit])
+        assert torch.equal(lse[0, 0, ~hit], clean[1][0, 0, ~hit])
