@@ -11,7 +11,11 @@ import torch
 from block_sparse_attention_34_b200 import autograd, paro
 from block_sparse_attention_34_b200.pipeline import Pipeline
 from oracle import paro_ref as ref
+from oracle import pasa_ref as pasa
+from oracle import selection_ref as sel
 from oracle import train_ref as tr
+
+from helpers import compare
 
 pytestmark = pytest.mark.gpu
 
@@ -220,3 +224,58 @@ def test_differentiable_on_a_table_larger_than_the_clip(dtype):
     assert abs(diff - (f64(g) * v).sum()) <= (bound * np.abs(v)).sum()
     with pytest.raises(ValueError, match="grid"):
         autograd.rope3d(x, table)
+
+
+@pytest.mark.parametrize("kw", [{}, {"int8": True}, {"baseline": True}, {"compensate": True},
+                                {"permuted": False}, {"selection": "hybrid", "top_p": 0.8, "window": 1}])
+def test_selection_sees_the_rotated_blocks(kw):
+    """attention(rope=...) and Pipeline keep the blocks that the means of the
+    rotated rows choose, of inputs whose scores lie more than 0.5 apart (and
+    whose unrotated means choose others), and compensate by those means."""
+    grid, d, heads, block, density = (6, 8, 21), 128, 3, 128, 0.3
+    orders = [0, 4, 8]
+    table = paro.RopeTable(grid, d)
+    pr = paro.Problem(1, heads, grid, d, block, orders)
+    rng = np.random.default_rng(7)
+    # along the pairs that turn fastest, two of each axis: unrotated, a block's
+    # rows point everywhere
+    way = np.zeros((heads, 1, 1, d))
+    fast = [2 * p + e for p in (0, 1, 22, 23, 43, 44) for e in (0, 1)]
+    way[..., fast] = np.sign(rng.standard_normal((heads, 1, 1, 12))) / 12 ** 0.5
+    way = torch.from_numpy(way).float().cuda()
+    size = torch.from_numpy(np.stack([rng.permutation(pr.NB) - 3.5 for _ in range(heads)])).float().cuda()
+    sign = torch.from_numpy(np.sign(rng.standard_normal((heads, pr.NB)))).float().cuda()
+
+    def clip(each, seed):  # rows whose rotated block means are each * way
+        y = 0.3 * random((heads, pr.NB, block, d), F32, seed)
+        y = (y - y.mean(2, keepdim=True) + each[..., None, None] * way).to(BF)
+        y = paro.inverse_reorder(y.view(pr.permuted), pr)
+        return paro.rope3d(y, table, inverse=True)
+
+    q, k, v = clip(4 * sign, 1), clip(3 * size, 2), random(pr.natural, BF, 3)
+    qr, kr = paro.rope3d(q, table), paro.rope3d(k, table)
+    _, _, scores = ref.pooled_scores(f64(qr), f64(kr), grid, orders, block)
+    assert np.diff(np.sort(scores, -1), axis=-1).min() > 0.5
+    count = ref.k_for_density(pr.NB, density)
+    if "selection" in kw:
+        want = sel.hybrid_select(scores, count, kw["top_p"], kw["window"])
+    else:
+        want = (ref.select_topk(scores, count),)
+
+    def same(kept):
+        kept = kept if isinstance(kept, tuple) else (kept,)
+        return all((a.cpu().numpy() == b).all() for a, b in zip(kept, want))
+
+    args = (grid, orders, block, density)
+    out, kept = paro.attention(q, k, v, *args, rope=table, **kw)
+    assert same(kept)
+    assert not same(paro.attention(q, k, v, *args, **kw)[1])
+    if "compensate" in kw:
+        compare(out, pasa.attention_compensated(f64(qr), f64(kr), f64(v), grid, orders, block, want[0]))
+        return
+    rotated, _ = paro.attention(qr, kr, v, *args, **kw)
+    assert torch.equal(out, rotated)
+    if "permuted" not in kw:
+        pipe = Pipeline(1, heads, grid, d, block, orders, density, rope=table, **kw)
+        assert torch.equal(pipe.run(q, k, v), rotated)
+        assert same((pipe.idx, pipe.counts) if "selection" in kw else pipe.idx)
