@@ -22,7 +22,7 @@
 // the tile (the scalar form, 16 lanes a key, took four times the
 // instructions and held a CTA at 46 GB/s).  P is not rounded to bf16 but
 // split, p = bf16(p) + rest, and both parts multiply V, so P V keeps 16 bits
-// of P: up to 8 query rows sit in rows 0-7 of the tile and the rests in rows
+// of P (off by 2^-16 at most; the sums are fp32): up to 8 query rows sit in rows 0-7 of the tile and the rests in rows
 // 8-15; with more, the rests are a second product.  fp32: one row a cluster,
 // fp32 arithmetic throughout.
 //

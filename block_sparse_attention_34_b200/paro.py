@@ -816,10 +816,13 @@ def block_sparse_query_attn(q, k, v, k_pool, pr: Problem, k_keep: int, lengths=N
 
     k, v [B, heads, N_p, d]: the clip in the permuted order, k_pool
     [B, heads, NB, d] float32 its block means (:func:`reorder` or
-    :func:`rope_reorder` with ``with_pool``); q_heads a multiple of heads
-    (query head h reads key head h // (q_heads / heads)).  ``lengths`` [B]
-    int32: how many positions of the order exist so far (0 .. N).  float32 or
-    bfloat16.  Returns (out [B, q_heads, M, d], idx [B, q_heads, M, k_keep]
+    :func:`rope_reorder` with ``with_pool``, for a whole clip); q_heads a
+    multiple of heads (query head h reads key head h // (q_heads / heads)).
+    ``lengths`` [B] int32: how many positions of the order exist so far
+    (0 .. N).  A clip that still grows has its means kept by the caller, over
+    the keys that exist: once position n - 1 is written, block j = (n - 1) //
+    block has ``k_pool[b, :, j] = k[b, :, j * block:n].float().mean(1)``.
+    float32 or bfloat16.  Returns (out [B, q_heads, M, d], idx [B, q_heads, M, k_keep]
     ascending with -1 behind the last, lse [B, q_heads, M]); a row without
     keys gives zeros and -inf."""
     i = _device_of(q)

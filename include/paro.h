@@ -514,22 +514,31 @@ PA_API pa_status pa_block_sparse_attn_backward(
 /* ---- Serving: single query tokens against a stored clip ---------------
  *
  * Query row m of head hq (key head hq / q_group): block scores q . k_pool_j
- * (held as two floats, some 46 bits; NaN read as -inf), the k_keep blocks with the largest
- * (ties to the lower index), softmax attention over their tokens:
+ * (held as two floats, some 46 bits; NaN read as -inf), the k_keep blocks with
+ * the largest (ties to the lower index), softmax attention over their tokens:
  *   out[b,hq,m,:] = sum_c softmax_c(q . k_c / sqrt(d)) v_c.
  * q, out [B, heads*q_group, M, d]; k, v [B,heads,N_p,d] in the permuted
  * order; k_pool [B,heads,NB,d] float, the blocks' mean keys; dtype PA_F32 or
- * PA_BF16, every product and sum in at least fp32.  lengths: NULL, or [B]
- * int32 device memory in [0, N]: only the first lengths[b] positions of the
- * order exist, blocks at or past them are no candidates and rows behind them
- * are never used (their k and v may hold anything); another value is
- * reported on dev_status (PA_ERR_DEVICE_CHECK) and its rows are left
- * unwritten.  idx [B,heads*q_group,M,k_keep] int32: the kept blocks,
- * ascending, -1 behind the last where fewer exist.  lse (may be NULL)
- * [B,heads*q_group,M] float: natural log-sum-exp of the row.  A row without
- * keys gives zeros and lse -inf.  1 <= k_keep <= NB <= 14528; M, q_group
- * >= 1; B*heads*q_group*M <= 2^27.  perms are not needed: shape's order is
- * the caller's. */
+ * PA_BF16.  PA_F32: fp32 products and sums.  PA_BF16: exact products and fp32
+ * sums of q . k and fp32 softmax statistics; the weights enter P V as two bf16
+ * halves (off by at most 2^-16 of the weight), whose exact products are summed
+ * in fp32.
+ * lengths: NULL, or [B] int32 device memory in [0, N]: only the first
+ * lengths[b] positions of the order exist, blocks at or past them are no
+ * candidates and rows behind them are never used (their k and v may hold
+ * anything); another value is reported on dev_status (PA_ERR_DEVICE_CHECK) and
+ * its rows are left unwritten.
+ * k_pool is the caller's to keep: with lengths, row j has to be the mean of the
+ * keys of block j that exist, rows j*block .. min((j+1)*block, lengths[b]) - 1.
+ * The pool outputs of pa_reorder and pa_rope_reorder are means over all N
+ * positions, right for whole blocks alone: the border block's score would count
+ * keys that do not exist, and where those hold NaN it would be -inf and the
+ * block dropped, newest keys and all.
+ * idx [B,heads*q_group,M,k_keep] int32: the kept blocks, ascending, -1 behind
+ * the last where fewer exist.  lse (may be NULL) [B,heads*q_group,M] float:
+ * natural log-sum-exp of the row.  A row without keys gives zeros and lse -inf.
+ * 1 <= k_keep <= NB <= 14528; M, q_group >= 1; B*heads*q_group*M <= 2^27.
+ * perms are not needed: shape's order is the caller's. */
 PA_API pa_status pa_query_attn(const void* q, const void* k, const void* v, const float* k_pool,
                                pa_dtype dtype, pa_shape shape, int32_t q_group, int32_t M,
                                int32_t k_keep, const int32_t* lengths, void* out, int32_t* idx,

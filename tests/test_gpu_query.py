@@ -236,3 +236,38 @@ def test_captured_and_concurrent_calls():
     for r in got:
         for a, b in zip(r, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("step", [1, 7, 64])
+def test_a_clip_that_grows(dtype, step):
+    """Keys, values and means arrive as documented, in a cache of NaN: the
+    oracle of the clip so far, whose newest keys are among the kept ones."""
+    c = Clip(1, 2, 2, 3, 64, 64, (3, 9, 11), dtype)
+    k, v, block = c.k.clone(), c.v.clone(), c.pr.block
+    for t in (c.k, c.v, c.pool):
+        t.fill_(float("nan"))
+    n = 0
+    while n < c.pr.N:
+        start, n = n, min(n + step, c.pr.N)
+        c.k[:, :, start:n], c.v[:, :, start:n] = k[:, :, start:n], v[:, :, start:n]
+        for j in range(start // block, (n - 1) // block + 1):
+            c.pool[:, :, j] = c.k[:, :, j * block:min((j + 1) * block, n)].float().mean(2)
+        if step > 1 or n % 13 in (0, 1) or n % block in (0, 1, 63) or n == c.pr.N:
+            exist = -(-n // block)
+            got = c.run(2, [n])
+            pool = np.zeros(c.pool.shape)
+            for j in range(exist):
+                pool[:, :, j] = f64(k)[:, :, j * block:min((j + 1) * block, n)].mean(2)
+            assert np.abs(f64(c.pool)[:, :, :exist] - pool[:, :, :exist]).max() <= 64 * 2.0 ** -24 * 8
+            want = tr.query_attention(f64(c.q), f64(k), f64(v), f64(c.pool), c.pr.N, block, 2, [n])
+            assert (got[1].cpu().numpy() == want[1]).all()
+            c_k, c_v = c.k, c.v
+            c.k, c.v = k, v  # the oracle reads nothing behind n
+            c.check(got, 2, [n])
+            c.k, c.v = c_k, c_v
+            # the newest block, made the best by its mean, is kept and read
+            q = c.q.clone()
+            c.q = c.pool[:, :, exist - 1].repeat_interleave(2, 1)[:, :, None].expand(q.shape).to(dtype).contiguous() * 8
+            assert (c.run(1, [n])[1] == exist - 1).all()
+            c.q = q
