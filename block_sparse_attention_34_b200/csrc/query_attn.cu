@@ -22,14 +22,16 @@
 // the tile (the scalar form, 16 lanes a key, took four times the
 // instructions and held a CTA at 46 GB/s).  P is not rounded to bf16 but
 // split, p = bf16(p) + rest, and both parts multiply V, so P V keeps 16 bits
-// of P (off by 2^-16 at most; the sums are fp32): up to 8 query rows sit in rows 0-7 of the tile and the rests in rows
-// 8-15; with more, the rests are a second product.  fp32: one row a cluster,
-// fp32 arithmetic throughout.
+// of P (off by 2^-16 at most; the sums are fp32): up to 8 query rows sit in
+// rows 0-7 of the tile and the rests in rows 8-15; with more, the rests are a
+// second product.  fp32: one row a cluster, fp32 arithmetic throughout.
 //
 // Measured: 12 heads' one row over 64 of 256 blocks (52 MB) 17.5 us, of which
 // some 9 are the launch, the scores' latency and the join, the rest at 6.5
 // TB/s; 40 heads' 16 rows each over 89 of 591 blocks (1.56 GB, each block read
 // once) 272 us, 5.7 TB/s.
+#include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "bwd.cuh"
@@ -44,8 +46,7 @@ using sm100::fmul2;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSms = 148;
-constexpr int kMaxCluster = 16;  // above 8 not portable, but every B200 has it
+constexpr int kMaxCluster = 16;  // above 8 not portable: asked for, see ClusterFit
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -838,14 +839,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// How many clusters of n[C] CTAs, one CTA an SM, the current device runs at
+// once (0: such a cluster does not fit): the driver's answer, asked for once a
+// device.  It depends on which SMs of the part are in use; one B200 of 148 SMs
+// runs 148, 74, 45, 33, 26, 22, 15, 15, 15, 11 and, from C = 11 on, 7.
+struct ClusterFit {
+  int n[kMaxCluster + 1];
+};
+template <auto Kern>
+cudaError_t cluster_fit(const ClusterFit** out) {
+  constexpr int kDevices = 64;
+  static std::atomic<const ClusterFit*> known[kDevices];
+  static ClusterFit fits[kDevices];
+  static std::mutex mutex;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kDevices) return cudaErrorInvalidDevice;
+  if ((*out = known[dev].load(std::memory_order_acquire)) != nullptr) return cudaSuccess;
+  const std::lock_guard<std::mutex> lock(mutex);
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, Kern)) != cudaSuccess) return e;
+  const int smem = kSmemOptIn - (int)fa.sharedSizeBytes;
+  if ((e = opt_in_smem<Kern, true>(smem)) != cudaSuccess) return e;
+  ClusterFit& fit = fits[dev];
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&fit.n[c], Kern, &cfg) != cudaSuccess) {
+      fit.n[c] = 0;
+      (void)cudaGetLastError();  // a size that does not fit is no error of the call
+    }
+  }
+  known[dev].store(&fit, std::memory_order_release);
+  *out = &fit;
+  return cudaSuccess;
+}
+
 template <typename T, int D, int kUnits>
 cudaError_t launch_units(const void* q, const void* k, const void* v, const float* k_pool,
                          const Grid& g, int per_head, int R, int C, int phase, int smem, int k_keep,
                          const int32_t* lengths, void* out, int32_t* idx, float* lse,
                          int32_t* status, cudaStream_t s) {
   auto kern = query_attn_kernel<T, D, kUnits>;
-  const cudaError_t e = opt_in_smem<query_attn_kernel<T, D, kUnits>, true>(smem);
-  if (e != cudaSuccess) return e;
   const int tiles = (per_head + R - 1) / R;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)g.B * g.heads * tiles * C));
@@ -878,22 +923,23 @@ cudaError_t launch_typed(const void* q, const void* k, const void* v, const floa
   const bool deep = kRingBytes<T, D, 6> + lists + kStatic <= kSmemOptIn;
   const int ring = deep ? kRingBytes<T, D, 6> : kRingBytes<T, D, 3>;
   const int room = kSmemOptIn - kStatic - lists;
+  const ClusterFit* fit = nullptr;
+  const cudaError_t e = deep ? cluster_fit<query_attn_kernel<T, D, 6>>(&fit)
+                             : cluster_fit<query_attn_kernel<T, D, 3>>(&fit);
+  if (e != cudaSuccess) return e;
   // rows of a cluster: as many as there are, but enough clusters for the SMs
   int R = per_head < kRows<T> ? per_head : kRows<T>;
   auto tiles = [&] { return (per_head + R - 1) / R; };
   auto front = [&] { return key_words(R, g.NB) * 8 + R * D * 4 + kWarps * 256 * 4; };
-  while (R > 1 && (heads * tiles() * kMaxCluster < kSms || front() > room)) R = (R + 1) / 2;
+  while (R > 1 && (heads * tiles() * kMaxCluster < fit->n[1] || front() > room)) R = (R + 1) / 2;
   // CTAs of a cluster: as many as let all clusters run at once, one CTA an
-  // SM (12 clusters of 12 CTAs, of which 7 fit, took 29 us, of 9 CTAs 18 us;
-  // kActive[C]: how many clusters of C fit, measured), but four means or a
-  // batch of 16 keys for each of their warps
-  static const int kActive[kMaxCluster + 1] = {0,  148, 74, 45, 33, 26, 22, 15, 15,
-                                               15, 11,  7,  7,  7,  7,  7,  7};
+  // SM (12 clusters of 12 CTAs, of which 7 fit, took 29 us, of 9 CTAs 18 us),
+  // but four means or a batch of 16 keys for each of their warps
   const int64_t items = (int64_t)k_keep * (g.block / 16);
   const int64_t useful = items / kWarps > g.NB / (4 * kWarps) ? items / kWarps : g.NB / (4 * kWarps);
   int C = 1;
   for (int c = 2; c <= kMaxCluster; ++c)
-    if (kActive[c] >= heads * tiles() && c <= useful) C = c;
+    if (fit->n[c] >= heads * tiles() && c <= useful) C = c;
   int phase = (int)((front() + 127) / 128 * 128);
   if (phase < ring) phase = ring;
   const int smem = phase + lists;

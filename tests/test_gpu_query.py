@@ -4,6 +4,10 @@ lse within the bounds of the roundings; one row to several clusters of them,
 shared key heads, lengths from none to all, garbage behind the end, ties,
 scores and values that are not finite, very many blocks."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -271,3 +275,32 @@ def test_a_clip_that_grows(dtype, step):
             c.q = c.pool[:, :, exist - 1].repeat_interleave(2, 1)[:, :, None].expand(q.shape).to(dtype).contiguous() * 8
             assert (c.run(1, [n])[1] == exist - 1).all()
             c.q = q
+
+
+FIRST_CALL = """
+import torch
+from block_sparse_attention_34_b200 import paro
+pr = paro.Problem(1, 3, (5, 9, 17), 128, 128, [0, 3, 5])
+for dtype in (torch.bfloat16, torch.float32):
+    k = torch.randn(pr.permuted, device="cuda").to(dtype)
+    pool = k.view(1, 3, pr.NB, 128, 128).float().mean(3)
+    q = torch.randn(1, 6, 2, 128, device="cuda").to(dtype)
+    out, idx, lse = (torch.empty_like(q), torch.empty(1, 6, 2, 3, dtype=torch.int32, device="cuda"),
+                     torch.empty(1, 6, 2, device="cuda"))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        paro.block_sparse_query_attn(q, k, k, pool, pr, 3, out=out, idx=idx, lse=lse)
+    graph.replay()
+    for a, b in zip((out, idx, lse), paro.block_sparse_query_attn(q, k, k, pool, pr, 3)):
+        assert torch.equal(a, b)
+print("fine")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """What the library asks the driver once a device is asked in a capture too."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert got.returncode == 0 and got.stdout.strip() == "fine", got.stderr[-2000:]
