@@ -213,7 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + kOffSlot);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* bad_flag = tmem_slot + 2;
-  volatile uint32_t* expired_flag = tmem_slot + 3;
   float* xch = reinterpret_cast<float*>(smem_raw + kOffX);
   float* s_alpha = reinterpret_cast<float*>(smem_raw + kOffA);
   float* s_cv = reinterpret_cast<float*>(smem_raw + kOffC);
@@ -268,9 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const bool malformed = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
-      *bad_flag = malformed;
-      *expired_flag =
-          status != nullptr && *reinterpret_cast<volatile int32_t*>(status) == PA_ERR_TIMEOUT;
+      *bad_flag = malformed || (status != nullptr && *reinterpret_cast<volatile int32_t*>(status) ==
+                                                        PA_ERR_TIMEOUT);
       if (malformed) report(status, PA_ERR_DEVICE_CHECK);
     }
   }
@@ -278,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const bool run = *bad_flag == 0 && *expired_flag == 0;
+  const bool run = *bad_flag == 0;
   const int n_tiles = run ? cnt : 0;
   const int row0 = (int)(bh * g.Np);
 
