@@ -858,6 +858,7 @@ cudaError_t cluster_fit(const ClusterFit** out) {
   if (dev >= kDevices) return cudaErrorInvalidDevice;
   if ((*out = known[dev].load(std::memory_order_acquire)) != nullptr) return cudaSuccess;
   const std::lock_guard<std::mutex> lock(mutex);
+  if ((*out = known[dev].load(std::memory_order_relaxed)) != nullptr) return cudaSuccess;
   cudaFuncAttributes fa;
   if ((e = cudaFuncGetAttributes(&fa, Kern)) != cudaSuccess) return e;
   const int smem = kSmemOptIn - (int)fa.sharedSizeBytes;
